@@ -265,6 +265,92 @@ int megamoe_set_overlap(int mode);
  * count written) when some were, MEGAMOE_EINVAL or MEGAMOE_EHIP otherwise. */
 int megamoe_last_error(const void *workspace, void *stream, int32_t *bad_route_count);
 
+/* ------------------------------------------------------------------------
+ * The router, the few-token layer and the MXFP4 expert path.  The pages take
+ * expert_idx and probs as given and run int8 experts; these entry points
+ * stand beside theirs, with the same conventions.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the arguments that take more than one. */
+typedef enum { MEGAMOE_FP32 = 0, MEGAMOE_FP16 = 1, MEGAMOE_BF16 = 2 } megamoe_type;
+
+/* Softmax top-k routing, which makes the expert_idx and probs of every forward:
+ *   score[t, e] = fp32(logits[t, e]) + bias[e]
+ * An expert whose score is NaN or -inf takes no part (a switched-off expert, a
+ * padded token).  The token's experts are the top_k largest scores, largest
+ * first; equal scores (+0 and -0 are equal) go to the lowest index first.
+ *   logits       logits_type [M, E]; the type's lowest finite value takes part
+ *   bias         nullable fp32 [E]: moves the choice, not the weights
+ *   renormalize  nonzero: probs = softmax of the chosen experts' logits; zero:
+ *                of the logits of all experts that take part.  Of logits that are
+ *                +inf each gets an equal share and finite ones 0.
+ *   expert_idx   int32 [M, top_k]; -1 where fewer than top_k experts take part
+ *                (the forwards drop such routes), with probs 0
+ *   probs        fp32 [M, top_k]
+ * Reads M, E and top_k of the dims. */
+int megamoe_route(const megamoe_dims *d, const void *logits, int logits_type, const float *bias,
+                  int renormalize, int32_t *expert_idx, float *probs, void *stream);
+
+/* megamoe_forward for a few tokens, M <= 16 and M * top_k <= 512 (else
+ * MEGAMOE_EUNSUPPORTED), in two kernels.  Arguments and result are those of
+ * megamoe_forward, bit for bit; a token may name an expert twice.  The workspace
+ * is small (megamoe_few_workspace_bytes) and needs no clearing; the dropped
+ * routes are read from it with megamoe_last_error. */
+int megamoe_few_workspace_bytes(const megamoe_dims *d, size_t *bytes);
+int megamoe_forward_few(const megamoe_dims *d, const uint16_t *x, const int32_t *expert_idx,
+                        const float *probs, const int8_t *w1p, const float *scale1,
+                        const int8_t *w2p, const float *scale2, uint16_t *out,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* MXFP4 rows (OCP Microscaling): 4-bit E2M1 elements (0, .5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives), 32 consecutive ones with an E8M0 scale byte b = 2^(b - 127).
+ *   q      uint8 [rows, cols / 2]   element 2 j in the low half of byte j
+ *   scale  uint8 [rows, cols / 32]
+ * Quantisation: the scale is 2^(floor(log2 max|x|) - 2), at least 2^-127; elements
+ * are x / scale to the nearest value, ties to the even code, larger ones to 6,
+ * the sign of x kept.  A block with a NaN or an infinity gets byte 255 (NaN) and
+ * codes 0.  Values read back are rounded to the output type; infinite where
+ * they pass its range.
+ *   x           type [rows, cols], cols a multiple of 32, rows * cols <= 2^36
+ *   valid_rows  nullable device int32 (4-byte aligned): only the first *valid_rows
+ *               rows are read and written, for example the last element of
+ *               expert_cumsum */
+int megamoe_mxfp4_quant(const void *x, int type, int64_t rows, int64_t cols,
+                        const int32_t *valid_rows, uint8_t *q, uint8_t *scale, void *stream);
+int megamoe_mxfp4_dequant(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                          const int32_t *valid_rows, void *x, int type, void *stream);
+
+/* The grouped products with MXFP4 rows and weights, summed in fp32.  Weights
+ * are rows over the reduction, one per output column, as megamoe_mxfp4_quant
+ * writes them, with no further layout:
+ *   w1q [E, 2I, K / 2], w1s [E, 2I, K / 32]   rows [0, I) feed silu, [I, 2I) the gate
+ *   w2q [E, K, I / 2],  w2s [E, K, I / 32]
+ * megamoe_mxfp4_gmm1 includes SwiGLU: for sorted row d of expert e's group, with
+ * x row sorted_route[d] / top_k (xq [M, K / 2], xs [M, K / 32], token-major),
+ *   p[n] = sum_k x[k] w1[e, n, k];  y[d, i] = bf16(silu(p[i]) * p[I + i])
+ * megamoe_mxfp4_gmm2: gmm2_out[d, n] = fp16(sum_i y[d, i] w2[e, n, i])
+ * (yq [R, I / 2], ys [R, I / 32] expert-major; fp16 is infinite past 65504).
+ * Groups are taken from expert_cumsum (device); rows at and past its last
+ * element are left as they are.  sorted_route and expert_cumsum come from any of
+ * the permute entry points.  The result does not depend on timing, but the
+ * order of the fp32 sum, and with it the last bits, depends on the dims. */
+int megamoe_mxfp4_gmm1(const megamoe_dims *d, const uint8_t *xq, const uint8_t *xs,
+                       const int32_t *sorted_route, const int32_t *expert_cumsum,
+                       const uint8_t *w1q, const uint8_t *w1s, uint16_t *y, void *stream);
+int megamoe_mxfp4_gmm2(const megamoe_dims *d, const uint8_t *yq, const uint8_t *ys,
+                       const int32_t *expert_cumsum, const uint8_t *w2q, const uint8_t *w2s,
+                       uint16_t *gmm2_out, void *stream);
+
+/* The whole layer with MXFP4 experts: route sort, megamoe_mxfp4_quant of x,
+ * megamoe_mxfp4_gmm1, megamoe_mxfp4_quant of y, megamoe_mxfp4_gmm2 and the combine
+ * of megamoe_unpermute (with no row scale).  x, expert_idx, probs and out as in
+ * megamoe_forward, dropped routes through megamoe_last_error. */
+int megamoe_mxfp4_workspace_bytes(const megamoe_dims *d, size_t *bytes);
+int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_t *expert_idx,
+                          const float *probs, const uint8_t *w1q, const uint8_t *w1s,
+                          const uint8_t *w2q, const uint8_t *w2s, uint16_t *out,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -92,6 +92,7 @@ hipError_t launch_swiglu_quant(const uint16_t *gmC, const float *pts1,
                                const int32_t *expert_cumsum, int R, int E, int I, int8_t *q2,
                                float *pts2, hipStream_t stream, const uint8_t *skip = nullptr,
                                const int32_t *prow = nullptr);
+// pts2 null: the rows are already in real units
 hipError_t launch_unpermute(const uint16_t *gmm2_out, const float *pts2,
                             const int32_t *expanded_row_idx, const float *probs, int M, int K,
                             int top_k, uint16_t *out, hipStream_t stream);
@@ -103,5 +104,50 @@ int gmm_pick_variant(int R, int E);
 // whether GMM1 at these dims can run SwiGLU in its last round (GmmParams tail_*)
 bool gmm_tail_ok(int R, int E, int I);
 hipError_t launch_gmm(int variant, const GmmParams &prm, int R, int cu_count, hipStream_t stream);
+
+
+// element types of the entry points that take more than one (megamoe_type)
+enum { kFp32 = 0, kFp16 = 1, kBf16 = 2 };
+
+// Softmax top-k (route.hip); bias nullable.
+hipError_t launch_route(const void *logits, int type, const float *bias, int M, int E, int top_k,
+                        int renormalize, int32_t *expert_idx, float *probs, hipStream_t stream);
+
+// The few-token layer (few.hip).
+constexpr int kFewMaxM = 16;
+struct FewParams {
+    const uint16_t *x;           // [M, K] fp16
+    const int32_t *expert_idx;   // [M, top_k]
+    const float *probs;          // [M, top_k]
+    const int8_t *w1p, *w2p;     // packed weights
+    const float *scale1, *scale2;
+    uint16_t *out;               // [M, K] bf16
+    int32_t *err;                // dropped routes
+    float *y;                    // scratch [R, I]: silu * gate of every (token, expert) pair
+    float *ymax;                 // scratch [R, I / 16]: its largest magnitude by 16 columns
+    int M, K, E, top_k, I;
+};
+bool few_ok(int M, int top_k);
+hipError_t launch_few(const FewParams &p, hipStream_t stream);
+
+// MXFP4 rows (mxfp4.hip).  valid_rows (nullable): a device count of the rows that hold data.
+hipError_t launch_mxfp4_quant(const void *x, int type, int64_t rows, int64_t cols,
+                              const int32_t *valid_rows, uint8_t *q, uint8_t *scale,
+                              hipStream_t stream);
+hipError_t launch_mxfp4_dequant(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                                const int32_t *valid_rows, void *x, int type, hipStream_t stream);
+
+// Grouped MXFP4 product (mxfp4_gmm.hip): the rows of expert e's group times its
+// weights.  With swiglu, w holds 2 N rows per expert and the output is bf16
+// silu(column n) * column N + n; without, w holds N rows and the output is fp16.
+struct MxGmmParams {
+    const uint8_t *a, *a_scale;  // [rows, Kred / 2] codes, [rows, Kred / 32] scales
+    const uint8_t *w, *w_scale;  // [E, N or 2 N, Kred / 2], [E, N or 2 N, Kred / 32]
+    const int32_t *a_route;      // nullable: A row d is row a_route[d] / a_div of a
+    const int32_t *cumsum;       // [E] inclusive row prefix over experts
+    uint16_t *c;                 // [R, N]
+    int R, E, N, Kred, a_div;
+};
+hipError_t launch_mxfp4_gmm(const MxGmmParams &p, bool swiglu, int cu_count, hipStream_t stream);
 
 }  // namespace megamoe

@@ -215,6 +215,70 @@ int permute_entry(const megamoe_dims *d, const uint16_t *x, const int32_t *exper
                        (hipStream_t)stream, (float *)(w + tsc), nullptr, nullptr, prow);
 }
 
+static_assert(kFp32 == MEGAMOE_FP32 && kFp16 == MEGAMOE_FP16 && kBf16 == MEGAMOE_BF16,
+              "the kernels' element types are the header's");
+
+bool type_ok(int type) {
+    return type == MEGAMOE_FP32 || type == MEGAMOE_FP16 || type == MEGAMOE_BF16;
+}
+
+// workspace of the few-token layer: the dropped-route word, y, its 16-column maxima
+struct FewLayout {
+    size_t y, ymax, total;
+};
+FewLayout few_layout(const megamoe_dims &d) {
+    const size_t R = (size_t)d.M * d.top_k;
+    FewLayout L;
+    L.y = align_up(kErrBytes);
+    L.ymax = L.y + align_up(R * d.I * 4);
+    L.total = L.ymax + align_up(R * (d.I / 16) * 4);
+    return L;
+}
+
+int check_few(const megamoe_dims *d) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    return few_ok(d->M, d->top_k) ? MEGAMOE_OK : MEGAMOE_EUNSUPPORTED;
+}
+
+// workspace of the MXFP4 forward
+struct Mxfp4Layout {
+    size_t err, bcnt, eri, sorted, counts, cumsum, xq, xs, y, yq, ys, g2, total;
+};
+Mxfp4Layout mxfp4_layout(const megamoe_dims &d) {
+    const size_t M = d.M, K = d.K, I = d.I, R = M * d.top_k;
+    Mxfp4Layout L;
+    size_t o = 0;
+    L.err = o;    o += align_up(kErrBytes);
+    L.bcnt = o;   o += align_up(route_sort_workspace_bytes((int)R, d.E));
+    L.eri = o;    o += align_up(R * 4);
+    L.sorted = o; o += align_up(R * 4);
+    L.counts = o; o += align_up((size_t)d.E * 4);
+    L.cumsum = o; o += align_up((size_t)d.E * 4);
+    L.xq = o;     o += align_up(M * (K / 2));
+    L.xs = o;     o += align_up(M * (K / 32));
+    L.y = o;      o += align_up(R * I * 2);
+    L.yq = o;     o += align_up(R * (I / 2));
+    L.ys = o;     o += align_up(R * (I / 32));
+    L.g2 = o;     o += align_up(R * K * 2);
+    L.total = o;
+    return L;
+}
+
+int run_mxfp4_gmm(const megamoe_dims &d, const uint8_t *a, const uint8_t *as, const int32_t *route,
+                  const int32_t *cumsum, const uint8_t *w, const uint8_t *ws, uint16_t *c,
+                  bool first, hipStream_t s) {
+    const MxGmmParams p{a, as, w, ws, route, cumsum, c, d.M * d.top_k, d.E,
+                        first ? d.I : d.K, first ? d.K : d.I, d.top_k};
+    return hip_status(launch_mxfp4_gmm(p, first, cu_count_current(), s));
+}
+
+// rows of MXFP4: whole blocks, and a grid below 2^32 threads
+int check_mxfp4_rows(int64_t rows, int64_t cols) {
+    if (rows < 1 || cols < 1) return MEGAMOE_EINVAL;
+    if (cols % 32 != 0 || cols > (1ll << 24) || rows > (1ll << 36) / cols)
+        return MEGAMOE_EUNSUPPORTED;
+    return MEGAMOE_OK;
+}
 
 }  // namespace
 
@@ -496,6 +560,123 @@ int megamoe_forward(const megamoe_dims *d, const uint16_t *x, const int32_t *exp
     MEGAMOE_TRY(run_gmm(*d, q2, cumsum, w2p, scale2, g2, nullptr, d->K, d->I, s, nullptr, nullptr,
                         true));
     return hip_status(launch_unpermute(g2, pts2, eri, probs, d->M, d->K, d->top_k, out, s));
+}
+
+int megamoe_route(const megamoe_dims *d, const void *logits, int logits_type, const float *bias,
+                  int renormalize, int32_t *expert_idx, float *probs, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {logits, expert_idx, probs};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if ((bias && !aligned16(bias)) || !type_ok(logits_type)) return MEGAMOE_EINVAL;
+    return hip_status(launch_route(logits, logits_type, bias, d->M, d->E, d->top_k,
+                                   renormalize != 0, expert_idx, probs, (hipStream_t)stream));
+}
+
+int megamoe_few_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
+    MEGAMOE_TRY(check_few(d));
+    if (!bytes) return MEGAMOE_EINVAL;
+    *bytes = few_layout(*d).total;
+    return MEGAMOE_OK;
+}
+
+int megamoe_forward_few(const megamoe_dims *d, const uint16_t *x, const int32_t *expert_idx,
+                        const float *probs, const int8_t *w1p, const float *scale1,
+                        const int8_t *w2p, const float *scale2, uint16_t *out, void *ws,
+                        size_t ws_bytes, void *stream) {
+    MEGAMOE_TRY(check_few(d));
+    const void *ptrs[] = {x, expert_idx, probs, w1p, scale1, w2p, scale2, out, ws};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    const FewLayout L = few_layout(*d);
+    if (ws_bytes < L.total) return MEGAMOE_EWORKSPACE;
+    char *base = (char *)ws;
+    const FewParams p{x, expert_idx, probs, w1p, w2p, scale1, scale2, out, (int32_t *)base,
+                      (float *)(base + L.y), (float *)(base + L.ymax), d->M, d->K, d->E, d->top_k,
+                      d->I};
+    return hip_status(launch_few(p, (hipStream_t)stream));
+}
+
+int megamoe_mxfp4_quant(const void *x, int type, int64_t rows, int64_t cols,
+                        const int32_t *valid_rows, uint8_t *q, uint8_t *scale, void *stream) {
+    MEGAMOE_TRY(check_mxfp4_rows(rows, cols));
+    const void *ptrs[] = {x, q, scale};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (((uintptr_t)valid_rows & 3u) != 0 || !type_ok(type)) return MEGAMOE_EINVAL;
+    return hip_status(
+        launch_mxfp4_quant(x, type, rows, cols, valid_rows, q, scale, (hipStream_t)stream));
+}
+
+int megamoe_mxfp4_dequant(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                          const int32_t *valid_rows, void *x, int type, void *stream) {
+    MEGAMOE_TRY(check_mxfp4_rows(rows, cols));
+    const void *ptrs[] = {q, scale, x};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (((uintptr_t)valid_rows & 3u) != 0 || !type_ok(type)) return MEGAMOE_EINVAL;
+    return hip_status(
+        launch_mxfp4_dequant(q, scale, rows, cols, valid_rows, x, type, (hipStream_t)stream));
+}
+
+int megamoe_mxfp4_gmm1(const megamoe_dims *d, const uint8_t *xq, const uint8_t *xs,
+                       const int32_t *sorted_route, const int32_t *expert_cumsum,
+                       const uint8_t *w1q, const uint8_t *w1s, uint16_t *y, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {xq, xs, sorted_route, expert_cumsum, w1q, w1s, y};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    return run_mxfp4_gmm(*d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, true,
+                         (hipStream_t)stream);
+}
+
+int megamoe_mxfp4_gmm2(const megamoe_dims *d, const uint8_t *yq, const uint8_t *ys,
+                       const int32_t *expert_cumsum, const uint8_t *w2q, const uint8_t *w2s,
+                       uint16_t *gmm2_out, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {yq, ys, expert_cumsum, w2q, w2s, gmm2_out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    return run_mxfp4_gmm(*d, yq, ys, nullptr, expert_cumsum, w2q, w2s, gmm2_out, false,
+                         (hipStream_t)stream);
+}
+
+int megamoe_mxfp4_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    if (!bytes) return MEGAMOE_EINVAL;
+    *bytes = mxfp4_layout(*d).total;
+    return MEGAMOE_OK;
+}
+
+int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_t *expert_idx,
+                          const float *probs, const uint8_t *w1q, const uint8_t *w1s,
+                          const uint8_t *w2q, const uint8_t *w2s, uint16_t *out, void *ws,
+                          size_t ws_bytes, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {x, expert_idx, probs, w1q, w1s, w2q, w2s, out, ws};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    const Mxfp4Layout L = mxfp4_layout(*d);
+    if (ws_bytes < L.total) return MEGAMOE_EWORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    char *base = (char *)ws;
+    int32_t *eri = (int32_t *)(base + L.eri);
+    int32_t *sorted = (int32_t *)(base + L.sorted);
+    int32_t *cumsum = (int32_t *)(base + L.cumsum);
+    uint8_t *xq = (uint8_t *)(base + L.xq), *xs = (uint8_t *)(base + L.xs);
+    uint16_t *y = (uint16_t *)(base + L.y), *g2 = (uint16_t *)(base + L.g2);
+    uint8_t *yq = (uint8_t *)(base + L.yq), *ys = (uint8_t *)(base + L.ys);
+    const int R = d->M * d->top_k;
+    MEGAMOE_TRY(hip_status(launch_route_sort(expert_idx, R, d->E, sorted, eri,
+                                             (int32_t *)(base + L.counts), cumsum,
+                                             (int32_t *)(base + L.err),
+                                             (int32_t *)(base + L.bcnt), s)));
+    MEGAMOE_TRY(hip_status(launch_mxfp4_quant(x, kFp16, d->M, d->K, nullptr, xq, xs, s)));
+    MEGAMOE_TRY(run_mxfp4_gmm(*d, xq, xs, sorted, cumsum, w1q, w1s, y, true, s));
+    MEGAMOE_TRY(hip_status(
+        launch_mxfp4_quant(y, kBf16, R, d->I, cumsum + d->E - 1, yq, ys, s)));
+    MEGAMOE_TRY(run_mxfp4_gmm(*d, yq, ys, nullptr, cumsum, w2q, w2s, g2, false, s));
+    return hip_status(launch_unpermute(g2, nullptr, eri, probs, d->M, d->K, d->top_k, out, s));
 }
 
 int megamoe_set_overlap(int mode) {

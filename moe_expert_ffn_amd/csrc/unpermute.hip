@@ -20,6 +20,9 @@ namespace megamoe {
 
 constexpr int kSlotBatch = 8;
 
+// SCALED false: the rows carry no scale (pts2 is not read), as after the MXFP4
+// GMM2, whose output is in real units.
+template <bool SCALED>
 __global__ __launch_bounds__(256) void unpermute_kernel(
     const uint16_t *__restrict__ gmm2_out, const float *__restrict__ pts2,
     const int32_t *__restrict__ expanded_row_idx, const float *__restrict__ probs, int K,
@@ -47,7 +50,7 @@ __global__ __launch_bounds__(256) void unpermute_kernel(
 #pragma unroll
         for (int u = 0; u < kSlotBatch; ++u) {
             if (d[u] >= 0) {  // d < 0: dropped route or past top_k
-                sc[u] = pts2[d[u]];
+                sc[u] = SCALED ? pts2[d[u]] : 1.0f;
                 // each GMM2 row is read once: non-temporal
                 raw[u] = load_nt16(gmm2_out + (size_t)d[u] * K + c * 8);
             }
@@ -81,8 +84,12 @@ hipError_t launch_unpermute(const uint16_t *gmm2_out, const float *pts2,
                             const int32_t *expanded_row_idx, const float *probs, int M, int K,
                             int top_k, uint16_t *out, hipStream_t stream) {
     dim3 grid(M, (K / 8 + 255) / 256), block(256);
-    hipLaunchKernelGGL(unpermute_kernel, grid, block, 0, stream, gmm2_out, pts2, expanded_row_idx,
-                       probs, K, top_k, out);
+    if (pts2)
+        hipLaunchKernelGGL(unpermute_kernel<true>, grid, block, 0, stream, gmm2_out, pts2,
+                           expanded_row_idx, probs, K, top_k, out);
+    else
+        hipLaunchKernelGGL(unpermute_kernel<false>, grid, block, 0, stream, gmm2_out, pts2,
+                           expanded_row_idx, probs, K, top_k, out);
     return hipGetLastError();
 }
 

@@ -43,7 +43,13 @@ EXPORTED = [
     "megamoe_unpermute", "megamoe_last_error", "megamoe_set_overlap",
     "megamoe_paired_q2_bytes", "megamoe_permute_tokens_paired", "megamoe_swiglu_quant_paired",
     "megamoe_gmm2_paired", "megamoe_gmm1_split_workspace_bytes", "megamoe_gmm1_gather_split",
+    "megamoe_route", "megamoe_few_workspace_bytes", "megamoe_forward_few", "megamoe_mxfp4_quant",
+    "megamoe_mxfp4_dequant", "megamoe_mxfp4_gmm1", "megamoe_mxfp4_gmm2",
+    "megamoe_mxfp4_workspace_bytes", "megamoe_forward_mxfp4",
 ]
+
+# megamoe_type: element types of the arguments that take more than one
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 _lib = None
 
@@ -97,6 +103,20 @@ def load() -> ctypes.CDLL:
     L.megamoe_swiglu_quant_paired.restype = i32
     L.megamoe_gmm2_paired.argtypes = [D, P, P, P, P, P, P, P]
     L.megamoe_gmm2_paired.restype = i32
+    i64 = ctypes.c_int64
+    L.megamoe_route.argtypes, L.megamoe_route.restype = [D, P, i32, P, i32, P, P, P], i32
+    L.megamoe_few_workspace_bytes.argtypes, L.megamoe_few_workspace_bytes.restype = [D, psz], i32
+    L.megamoe_forward_few.argtypes = [D, P, P, P, P, P, P, P, P, P, sz, P]
+    L.megamoe_forward_few.restype = i32
+    L.megamoe_mxfp4_quant.argtypes, L.megamoe_mxfp4_quant.restype = [P, i32, i64, i64, P, P, P, P], i32
+    L.megamoe_mxfp4_dequant.argtypes = [P, P, i64, i64, P, P, i32, P]
+    L.megamoe_mxfp4_dequant.restype = i32
+    L.megamoe_mxfp4_gmm1.argtypes, L.megamoe_mxfp4_gmm1.restype = [D, P, P, P, P, P, P, P, P], i32
+    L.megamoe_mxfp4_gmm2.argtypes, L.megamoe_mxfp4_gmm2.restype = [D, P, P, P, P, P, P, P], i32
+    L.megamoe_mxfp4_workspace_bytes.argtypes = [D, psz]
+    L.megamoe_mxfp4_workspace_bytes.restype = i32
+    L.megamoe_forward_mxfp4.argtypes = [D, P, P, P, P, P, P, P, P, P, sz, P]
+    L.megamoe_forward_mxfp4.restype = i32
     _lib = L
     return L
 
@@ -299,6 +319,133 @@ def megamoe_last_error(workspace, stream=None) -> int:
     if rc != MEGAMOE_EDEVICE:
         _check("megamoe_last_error", rc)
     return v.value
+
+
+def _type(t: torch.Tensor) -> int:
+    if t.dtype not in _TYPES:
+        raise TypeError(f"expected one of {sorted(map(str, _TYPES))}, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _shape(name: str, t: torch.Tensor, *shape: int) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, stream=None):
+    _shape("logits", logits, d.M, d.E)
+    _shape("expert_idx", expert_idx, d.M, d.top_k)
+    _shape("probs", probs, d.M, d.top_k)
+    if bias is not None:
+        _shape("bias", bias, d.E)
+    _check("megamoe_route", load().megamoe_route(
+        ctypes.byref(d), _ptr(logits), _type(logits), _ptr(bias, torch.float32),
+        int(bool(renormalize)), _ptr(expert_idx, torch.int32), _ptr(probs, torch.float32),
+        _stream(stream)))
+
+
+def megamoe_few_workspace_bytes(d: megamoe_dims) -> int:
+    n = ctypes.c_size_t(0)
+    _check("megamoe_few_workspace_bytes",
+           load().megamoe_few_workspace_bytes(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def megamoe_forward_few(d, x, expert_idx, probs, w1p, scale1, w2p, scale2, out, workspace,
+                        stream=None):
+    _shape("x", x, d.M, d.K)
+    _shape("expert_idx", expert_idx, d.M, d.top_k)
+    _shape("probs", probs, d.M, d.top_k)
+    _shape("out", out, d.M, d.K)
+    _check("megamoe_forward_few", load().megamoe_forward_few(
+        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
+        _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
+        _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(out, torch.bfloat16),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _rows_cols(x: torch.Tensor) -> tuple[int, int]:
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [rows, cols], got {tuple(x.shape)}")
+    return tuple(x.shape)
+
+
+def _mx_rows(q: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, valid_rows) -> None:
+    _shape("q", q, rows, cols // 2)
+    _shape("scale", scale, rows, cols // 32)
+    if valid_rows is not None and valid_rows.numel() != 1:
+        raise ValueError("valid_rows: expected one element")
+
+
+def megamoe_mxfp4_quant(x, q, scale, valid_rows=None, stream=None):
+    """x [rows, cols] fp32, fp16 or bf16 -> q uint8 [rows, cols / 2], scale uint8
+    [rows, cols / 32].  valid_rows: int32 device tensor of one element."""
+    rows, cols = _rows_cols(x)
+    _mx_rows(q, scale, rows, cols, valid_rows)
+    _check("megamoe_mxfp4_quant", load().megamoe_mxfp4_quant(
+        _ptr(x), _type(x), rows, cols, _ptr(valid_rows, torch.int32), _ptr(q, torch.uint8),
+        _ptr(scale, torch.uint8), _stream(stream)))
+
+
+def megamoe_mxfp4_dequant(q, scale, x, valid_rows=None, stream=None):
+    rows, cols = _rows_cols(x)
+    _mx_rows(q, scale, rows, cols, valid_rows)
+    _check("megamoe_mxfp4_dequant", load().megamoe_mxfp4_dequant(
+        _ptr(q, torch.uint8), _ptr(scale, torch.uint8), rows, cols,
+        _ptr(valid_rows, torch.int32), _ptr(x), _type(x), _stream(stream)))
+
+
+def _mx_weights(name: str, d, q: torch.Tensor, s: torch.Tensor, rows: int, cols: int) -> None:
+    _shape(name + "q", q, d.E, rows, cols // 2)
+    _shape(name + "s", s, d.E, rows, cols // 32)
+
+
+def megamoe_mxfp4_gmm1(d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, stream=None):
+    R = d.M * d.top_k
+    _mx_rows(xq, xs, d.M, d.K, None)
+    _shape("sorted_route", sorted_route, R)
+    _shape("expert_cumsum", expert_cumsum, d.E)
+    _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
+    _shape("y", y, R, d.I)
+    _check("megamoe_mxfp4_gmm1", load().megamoe_mxfp4_gmm1(
+        ctypes.byref(d), _ptr(xq, torch.uint8), _ptr(xs, torch.uint8),
+        _ptr(sorted_route, torch.int32), _ptr(expert_cumsum, torch.int32),
+        _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8), _ptr(y, torch.bfloat16),
+        _stream(stream)))
+
+
+def megamoe_mxfp4_gmm2(d, yq, ys, expert_cumsum, w2q, w2s, gmm2_out, stream=None):
+    R = d.M * d.top_k
+    _mx_rows(yq, ys, R, d.I, None)
+    _shape("expert_cumsum", expert_cumsum, d.E)
+    _mx_weights("w2", d, w2q, w2s, d.K, d.I)
+    _shape("gmm2_out", gmm2_out, R, d.K)
+    _check("megamoe_mxfp4_gmm2", load().megamoe_mxfp4_gmm2(
+        ctypes.byref(d), _ptr(yq, torch.uint8), _ptr(ys, torch.uint8),
+        _ptr(expert_cumsum, torch.int32), _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8),
+        _ptr(gmm2_out, torch.float16), _stream(stream)))
+
+
+def megamoe_mxfp4_workspace_bytes(d: megamoe_dims) -> int:
+    n = ctypes.c_size_t(0)
+    _check("megamoe_mxfp4_workspace_bytes",
+           load().megamoe_mxfp4_workspace_bytes(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def megamoe_forward_mxfp4(d, x, expert_idx, probs, w1q, w1s, w2q, w2s, out, workspace,
+                          stream=None):
+    _shape("x", x, d.M, d.K)
+    _shape("expert_idx", expert_idx, d.M, d.top_k)
+    _shape("probs", probs, d.M, d.top_k)
+    _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
+    _mx_weights("w2", d, w2q, w2s, d.K, d.I)
+    _shape("out", out, d.M, d.K)
+    _check("megamoe_forward_mxfp4", load().megamoe_forward_mxfp4(
+        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
+        _ptr(probs, torch.float32), _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8),
+        _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8), _ptr(out, torch.bfloat16),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def megamoe_set_overlap(mode: int) -> None:
