@@ -70,4 +70,13 @@ __device__ __forceinline__ int wave_inclusive_scan(int v) {
     return v;
 }
 
+// A wave-uniform pointer, kept in scalar registers.
+template <typename T>
+__device__ __forceinline__ const T *uniform_ptr(const T *p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const T *)((uint64_t)hi << 32 | lo);
+}
+
 }  // namespace megamoe

@@ -47,4 +47,15 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
 
+// One dword per lane, global -> LDS (lane i writes LDS bytes [lds_base + 4 i,
+// lds_base + 4 i + 4)).
+__device__ __forceinline__ void dma4(const void *gptr, uint32_t lds_base) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "global_load_lds_dword %1, off"
+        :
+        : "s"(lds_base), "v"(gptr)
+        : "memory", "m0");
+}
+
 }  // namespace megamoe

@@ -92,14 +92,6 @@ __device__ __forceinline__ int few_group(int b, int n) {
     return (n & 7) ? b : (b & 7) * (n >> 3) + (b >> 3);
 }
 
-// A wave-uniform pointer, kept in scalar registers.
-__device__ __forceinline__ const int8_t *few_uniform(const int8_t *p) {
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const int8_t *)((uint64_t)hi << 32 | lo);
-}
-
 // 16 bytes of a wave-uniform block at the lane's offset
 __device__ __forceinline__ v4i few_load(const int8_t *block, uint32_t off) {
     typedef const __attribute__((address_space(1))) v4i *global_v4i;
@@ -175,16 +167,16 @@ few_gmm1_kernel(FewParams p, int row_cap) {
         auto seek = [&](int nu) {
             const int ng = I + nu;
             const int8_t *first = we + (size_t)s0 * slice;
-            qu = few_uniform(first + (size_t)(nu / kPackRowsF) * kPackBlockF + (nu % kPackRowsF) * 64);
-            qg = few_uniform(first + (size_t)(ng / kPackRowsF) * kPackBlockF + (ng % kPackRowsF) * 64);
+            qu = uniform_ptr(first + (size_t)(nu / kPackRowsF) * kPackBlockF + (nu % kPackRowsF) * 64);
+            qg = uniform_ptr(first + (size_t)(ng / kPackRowsF) * kPackBlockF + (ng % kPackRowsF) * 64);
             li = 0;
         };
         auto load = [&](int u) {
             fu[u] = few_load(qu, woff);
             fg[u] = few_load(qg, woff);
             const size_t step = ++li < cnt ? slice : 0;
-            qu = few_uniform(qu + step);
-            qg = few_uniform(qg + step);
+            qu = uniform_ptr(qu + step);
+            qg = uniform_ptr(qg + step);
         };
         seek(nu0);
 #pragma unroll
@@ -360,7 +352,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
         t1 = (hw + 1) * T / kFew2Waves;
     };
     auto expert = [&]() {
-        lq = few_uniform(w0 + (size_t)(to.i0 / 64 + ls) * slice + s_p.act[la] * block);
+        lq = uniform_ptr(w0 + (size_t)(to.i0 / 64 + ls) * slice + s_p.act[la] * block);
     };
     auto seek = [&](const FewStep &t) {  // a step with experts
         to = t;
@@ -380,7 +372,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
                 ++la;
                 expert();
             } else {
-                lq = few_uniform(lq + slice);
+                lq = uniform_ptr(lq + slice);
             }
         }
     };

@@ -177,17 +177,6 @@ __device__ __forceinline__ int lds_off64s(int row, int chunk) {
     return row * kBK64 + ((chunk ^ swz64(row)) << 4);
 }
 
-// One dword per lane, global -> LDS (lane i writes LDS bytes [lds_base + 4 i,
-// lds_base + 4 i + 4)); used for the per-channel scales of a tile.
-__device__ __forceinline__ void dma4(const void *gptr, uint32_t lds_base) {
-    asm volatile(
-        "s_mov_b32 m0, %0\n\t"
-        "global_load_lds_dword %1, off"
-        :
-        : "s"(lds_base), "v"(gptr)
-        : "memory", "m0");
-}
-
 // ---------------------------------------------------------------------------
 // Ring pipeline.  A stage is one 64-byte K slice of the tile's BM A rows and
 // BN weight rows ([BM + BN rows][64 B], swizzled as above), copied by DMA

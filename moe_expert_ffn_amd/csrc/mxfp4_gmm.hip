@@ -189,10 +189,12 @@ static void launch_stream(const MxGmmParams &p, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows per expert: 256 x 256 tiles on the matrix cores.  Four waves, one to
-// a SIMD, each multiply all rows of the tile by 64 of its columns, so that the
-// time of a tile follows its live rows in steps of 32 and no wave idles in a
-// ragged one; 16 x 4 fragments of sums fill half of the register file.
+// Many rows per expert: tiles of 256 rows by 256 weight rows on the matrix cores.
+// Four waves, one to a SIMD, each multiply all rows of the tile by 64 of its
+// weight rows, so that the time of a tile follows its live rows in steps of 64 and
+// no wave idles in a ragged one; 8 x 2 fragments of 32 x 32 sums fill half of the
+// register file.  (v_mfma_scale_f32_32x32x64_f8f6f4 ran at 9.3 PFLOP/s from registers,
+// the 16x16x128 form at 5.5.)
 //
 // A stage is 128 of the reduction: 64 bytes of codes of 256 rows and 256 weight
 // rows, copied asynchronously into a ring of four stages in LDS.  The scales of
@@ -201,62 +203,98 @@ static void launch_stream(const MxGmmParams &p, hipStream_t stream) {
 // multiplied: behind it the copies of stage s + 3 start (into the slot of stage
 // s - 1, which every wave has read) and the first fragments of stage s + 1 are
 // read, so that the matrix cores do not wait at a stage's start.
+//
+// The grid is persistent.  While a tile is multiplied the workgroup looks up its
+// next one, and the first three stages of that are copied while this one's sums
+// are rounded and stored.
 constexpr int kMxTile = 256;                    // rows, and weight rows
 constexpr int kMxRing = 4;
 constexpr int kMxStageBytes = 2 * kMxTile * 64; // rows then weight rows
 constexpr int kMxScaleBytes = 2 * kMxTile * 16;
+constexpr int kMxTileThreads = 256;
+constexpr int kMxE = 256;
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// 32 x 32 x 64 with weights as the first operand: lane l holds output row l & 31 and
+// the columns 8 q + 4 (l >> 5) + 0..3, q = 0..3.  Of either operand lane l has row
+// l & 31 and the codes of block l >> 5; their scale is byte 2 H of the scale word.
+template <int H>
+__device__ __forceinline__ v16f mx_mfma32(v4i w, int ws, v4i a, int as, v16f acc) {
+    const v8i w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc, 4, 4, 2 * H, ws, 2 * H, as);
+}
 
 // 16-byte chunk c of a 64-byte row: the place without bank conflicts for reads of
-// one chunk index of 16 consecutive rows by each lane group
+// one chunk index of consecutive rows by each lane group
 __device__ __forceinline__ int mx_swz(int row, int c) { return c ^ ((row >> 1) & 3); }
+
+// The tiles, numbered by expert, weight block and row block; an expert's rows are
+// split evenly over its row blocks in units of 32.
+struct MxSchedule {
+    int pre[kMxE + 1];  // tiles of the experts before e
+    int first[kMxE], rows[kMxE];
+    int total;
+};
+__device__ __forceinline__ void mx_schedule(const MxGmmParams &p, int NB, int *s_w, MxSchedule &s) {
+    const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
+    const int first = e < p.E ? mx_row_end(p, e - 1) : 0;
+    const int rows = e < p.E ? max(0, mx_row_end(p, e) - first) : 0;
+    const int tiles = (rows + kMxTile - 1) / kMxTile * NB;
+    const int incl = wave_inclusive_scan(tiles);
+    if (lane == kWave - 1) s_w[wave] = incl;
+    __syncthreads();
+    int pre = incl - tiles;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) pre += w < wave ? s_w[w] : 0;
+    s.pre[e] = pre;  // experts past E have no tiles: pre is the total
+    s.first[e] = first;
+    s.rows[e] = rows;
+    if (e == kMxE - 1) s.pre[kMxE] = s.total = pre + tiles;
+    __syncthreads();
+}
 
 struct MxTile {
     int e, row0, rows, nblk;
 };
-
-// Tile t of the schedule: by expert, weight block, row block, an expert's rows
-// split evenly over its row blocks in units of 16.  e = -1 past the last tile.
-__device__ __forceinline__ MxTile mx_find_tile(const MxGmmParams &p, int NB, int pid, int (*s_w)[4],
-                                               MxTile *s_t) {
-    const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
-    const int first = e < p.E ? mx_row_end(p, e - 1) : 0;
-    const int rows = e < p.E ? max(0, mx_row_end(p, e) - first) : 0;
-    const int mb = (rows + kMxTile - 1) / kMxTile;
-    const int incl = wave_inclusive_scan(mb * NB);
-    if (lane == kWave - 1) s_w[0][wave] = incl;
-    if (e == 0) s_t->e = -1;
-    __syncthreads();
-    int pre = incl - mb * NB, total = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        pre += w < wave ? s_w[0][w] : 0;
-        total += s_w[0][w];
+__device__ __forceinline__ MxTile mx_find_tile(const MxSchedule &s, int t) {  // t < total
+    int lo = 0, hi = kMxE - 1;  // the last expert that starts at or before t and has tiles
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s.pre[mid + 1] > t) hi = mid;
+        else lo = mid + 1;
     }
-    // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share
-    // weight and row blocks in its L2
-    const int per = (total + 7) / 8, at = pid >> 3;
-    const int t = (pid & 7) * per + at;
-    if (at < per && t >= pre && t < pre + mb * NB) {
-        const int local = t - pre, m = local % mb;
-        const int nu = (rows + 15) / 16, q = nu / mb, r = nu % mb;
-        const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
-        *s_t = MxTile{e, first + 16 * u0, min(rows, 16 * u1) - 16 * u0, local / mb};
-    }
-    __syncthreads();
-    return *s_t;
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int rows = __builtin_amdgcn_readfirstlane(s.rows[e]);
+    const int local = t - __builtin_amdgcn_readfirstlane(s.pre[e]);
+    const int mb = (rows + kMxTile - 1) / kMxTile, m = local % mb;
+    const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
+    const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
+    return MxTile{e, __builtin_amdgcn_readfirstlane(s.first[e] + 32 * u0),
+                  __builtin_amdgcn_readfirstlane(min(rows, 32 * u1) - 32 * u0),
+                  __builtin_amdgcn_readfirstlane(local / mb)};
 }
 
-// One tile of at most 32 NP rows.  (One body for every NP, with the row pairs behind
-// conditions, made the compiler move the sums between register files.)
-template <bool SWIGLU, int NP>
-__device__ __forceinline__ void mx_tile(const MxGmmParams &p, int e, int row0, int rows, int n0,
-                                        uint8_t *s_data, uint8_t *s_scale) {
+// What the copies of a tile need.
+struct MxCopies {
+    uint32_t voff_a[4], voff_w[4], soff_a, soff_w;  // per lane
+    const uint8_t *wq, *ws;                         // the expert's weights and scales
+    int ac;                                         // copies of 16 rows a wave makes, rows / 64
+};
+
+struct MxLds {
+    uint8_t *data, *scale;
+    uint32_t data_at, scale_at;  // their LDS addresses
+    int32_t *route;              // [256] A rows of the next tile, as sorted routes
+};
+
+template <bool SWIGLU>
+__device__ __forceinline__ MxCopies mx_copies(const MxGmmParams &p, const MxTile &t, const MxLds &l) {
     constexpr int F = SWIGLU ? 2 : 1;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ns = p.Kred / 128;
     const uint32_t qrow = p.Kred / 2, srow = p.Kred / 32;
-
+    const int n0 = t.nblk * (kMxTile / F);
     // tile weight row r -> weight row of the expert: wave w's 64 are, with SwiGLU, 32 silu
     // columns and the 32 gate columns that go with them
     auto weight_row = [&](int r) {
@@ -264,182 +302,291 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, int e, int row0, i
         const int col = SWIGLU ? n0 + 32 * w + (c & 31) : n0 + r;
         return min(col, p.N - 1) + (SWIGLU && c >= 32 ? p.N : 0);
     };
-    auto data_row = [&](int r) { return (uint32_t)mx_a_row(p, row0 + min(r, rows - 1)); };
-    const uint8_t *wq = p.w + (size_t)e * p.N * F * qrow, *ws = p.w_scale + (size_t)e * p.N * F * srow;
-    // this wave's copies of a stage: AC of 16 rows and four of 16 weight rows, 1 KB each
-    constexpr int AC = NP / 2;
-    uint32_t voff_a[AC], voff_w[4];
-#pragma unroll
-    for (int i = 0; i < AC; ++i) {
-        const int r = (wave * AC + i) * 16 + (lane >> 2);
-        voff_a[i] = data_row(r) * qrow + mx_swz(r, lane & 3) * 16;
-    }
+    auto data_row = [&](int r) {
+        r = min(r, t.rows - 1);
+        if (!p.a_route) return t.row0 + r;
+        const int v = l.route[r];
+        return (v < 0 ? 0 : v < p.R ? v : p.R - 1) / p.a_div;
+    };
+    MxCopies c;
+    c.ac = (t.rows + 63) / 64;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = (wave * 4 + i) * 16 + (lane >> 2);
-        voff_w[i] = weight_row(r) * qrow + mx_swz(r, lane & 3) * 16;
+        const int r = (wave * c.ac + i) * 16 + (lane >> 2);
+        c.voff_a[i] = (uint32_t)data_row(i < c.ac ? r : 0) * qrow + mx_swz(r, lane & 3) * 16;
+        const int n = (wave * 4 + i) * 16 + (lane >> 2);
+        c.voff_w[i] = (uint32_t)weight_row(n) * qrow + mx_swz(n, lane & 3) * 16;
     }
-    const uint32_t soff_a = data_row(wave * 64 + lane) * srow;
-    const uint32_t soff_w = weight_row(wave * 64 + lane) * srow;
-    const uint32_t data_lds = __builtin_amdgcn_readfirstlane(lds_addr(s_data));
-    const uint32_t scale_lds = __builtin_amdgcn_readfirstlane(lds_addr(s_scale));
+    c.soff_a = (uint32_t)data_row(wave * 64 + lane) * srow;
+    c.soff_w = (uint32_t)weight_row(wave * 64 + lane) * srow;
+    c.wq = uniform_ptr(p.w + (size_t)t.e * p.N * F * qrow);
+    c.ws = uniform_ptr(p.w_scale + (size_t)t.e * p.N * F * srow);
+    return c;
+}
 
-    // the 16 scale bytes of stages 4 c .. 4 c + 3; the last ones start early so as to end with the row
-    auto scale_start = [&](int c) { return min(16 * c, (int)srow - 16); };
-    auto issue = [&](int s) {
-        if ((s & 3) == 0) {
-            const int c = s >> 2;
-            const uint32_t at = scale_lds + (c & 1) * kMxScaleBytes + wave * 1024;
-            dma16(p.a_scale + scale_start(c), soff_a, at);
-            dma16(ws + scale_start(c), soff_w, at + kMxTile * 16);
-        }
-        const uint32_t at = data_lds + (s & 3) * kMxStageBytes;
-        const uint8_t *ga = p.a + (size_t)s * 64, *gw = wq + (size_t)s * 64;
-#pragma unroll
-        for (int i = 0; i < AC; ++i) dma16(ga, voff_a[i], at + (wave * AC + i) * 1024);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dma16(gw, voff_w[i], at + kMxTile * 64 + (wave * 4 + i) * 1024);
-    };
+// where the 16 scale bytes of stages 4 c .. 4 c + 3 start in a row of n; the last ones start
+// early so as to end with the row
+__device__ __forceinline__ int mx_scale_start(int c, int n) { return min(16 * c, n - 16); }
 
-    const int r = lane & 15, g = lane >> 4;
-    // lane's place in a fragment of 16 rows, of codes and of scales
-    const int frag_off = r * 64 + mx_swz(r, g) * 16, scale_off = r * 16 + g;
-    struct Pair {  // two row fragments
-        v4i f[2];
-        int s[2];
-    };
-    struct Weights {
-        v4i f[4];
-        int s[4];
-    };
-    auto scales = [&](int s) {  // of stage s, of tile row 0
-        const int c = s >> 2;
-        return s_scale + (c & 1) * kMxScaleBytes + scale_off + 4 * s - scale_start(c);
-    };
-    auto codes = [&](int s) { return s_data + (s & 3) * kMxStageBytes + frag_off; };
-    auto read_w = [&](int s) {
-        Weights w;
-        const uint8_t *q = codes(s) + (kMxTile + wave * 64) * 64;
-        const uint8_t *x = scales(s) + (kMxTile + wave * 64) * 16;
+// The copies of stage s: at every fourth stage 2 of scales, then ac of rows and 4 of
+// weight rows.  AC: ac where it is known (0: not).
+template <int AC>
+__device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies &c, const MxLds &l, int s) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ac = AC ? AC : c.ac;
+    if ((s & 3) == 0) {
+        const int k = s >> 2, start = mx_scale_start(k, p.Kred / 32);
+        const uint32_t at = l.scale_at + (k & 1) * kMxScaleBytes + wave * 1024;
+        dma16(uniform_ptr(p.a_scale + start), c.soff_a, at);
+        dma16(uniform_ptr(c.ws + start), c.soff_w, at + kMxTile * 16);
+    }
+    const uint32_t at = l.data_at + (s & 3) * kMxStageBytes;
+    const uint8_t *ga = uniform_ptr(p.a + (size_t)s * 64), *gw = uniform_ptr(c.wq + (size_t)s * 64);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w.f[j] = *reinterpret_cast<const v4i *>(q + 16 * j * 64);
-            w.s[j] = x[16 * j * 16];
-        }
-        return w;
-    };
-    auto read_a = [&](const uint8_t *q, const uint8_t *x, int pair) {
-        Pair a;
+    for (int i = 0; i < (AC ? AC : 4); ++i)
+        if (AC || i < ac) dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            a.f[h] = *reinterpret_cast<const v4i *>(q + (32 * pair + 16 * h) * 64);
-            a.s[h] = x[(32 * pair + 16 * h) * 16];
-        }
-        return a;
+    for (int i = 0; i < 4; ++i) dma16(gw, c.voff_w[i], at + kMxTile * 64 + (wave * 4 + i) * 1024);
+}
+
+// silu(u) * g for a result that is rounded to bf16: the reciprocal's last ulp is not corrected
+__device__ __forceinline__ float mx_silu_times(float u, float g) {
+    const float d = __builtin_amdgcn_exp2f(u * -1.4426950408889634f) + 1.0f;
+    return u * __builtin_amdgcn_rcpf(d) * g;
+}
+
+// One sum out of the accumulation registers.  (Left to the compiler, all 256 are copied
+// at once and other values spill.)
+__device__ __forceinline__ float mx_sum(float a) {
+    float v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+}
+
+// Multiplies tile t, of at most 32 NP rows, whose first three stages are in LDS, rounds its
+// sums, and stores them while the first stages of tile `nt` are copied.  (One body for every NP, with the rows behind
+// conditions, made the compiler move the sums between register files.)
+template <bool SWIGLU, int NP>
+__device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies &c,
+                                        bool more, const MxTile &nt, const MxLds &l) {
+    constexpr int F = SWIGLU ? 2 : 1, AC = NP / 2;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ns = p.Kred / 128;
+
+    const int r = lane & 31, g = lane >> 5;
+    const int frag_off[2] = {r * 64 + mx_swz(r, g) * 16, r * 64 + mx_swz(r, 2 + g) * 16};
+    // LDS addresses of stage s, tile row 0
+    auto codes = [&](int s) { return l.data + (s & 3) * kMxStageBytes; };
+    auto scales = [&](int s) {
+        const int k = s >> 2;
+        return l.scale + (k & 1) * kMxScaleBytes + r * 16 + 4 * s - mx_scale_start(k, p.Kred / 32);
     };
-    v4f acc[2 * NP][4] = {};
-    auto multiply = [&](int pair, const Pair &a, const Weights &w) {
+    // 32 rows of a stage: two fragments, and the rows' four scale bytes
+    auto read = [&](const uint8_t *q, const uint8_t *x, int row, v4i (&f)[2], int &sc) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
+            f[h] = *reinterpret_cast<const v4i *>(q + row * 64 + frag_off[h]);
+        sc = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
+    };
+    auto read_w = [&](int s, v4i (&f)[2][2], int (&sc)[2]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[2 * pair + h][j] = mx_mfma(w.f[j], w.s[j], a.f[h], a.s[h], acc[2 * pair + h][j]);
+        for (int j = 0; j < 2; ++j)
+            read(codes(s), scales(s), kMxTile + wave * 64 + 32 * j, f[j], sc[j]);
+    };
+    v16f acc[NP][2] = {};
+    v4i w[2][2], a[2];  // weights of the stage, rows of the fragment that is multiplied
+    int wsc[2], asc;
+    auto multiply = [&](int i) {
+        const int as = asc >> (8 * g);  // the lane's blocks are g and 2 + g
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma32<0>(w[j][0], wsc[j], a[0], as, acc[i][j]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma32<1>(w[j][1], wsc[j], a[1], as, acc[i][j]);
+        // the sums are wanted here: without this the compiler puts a stage's products together
+        // behind its barrier and copies, where the reads no longer overlap them
+#pragma unroll
+        for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[i][j]));
     };
 
-    issue(0);
-    issue(1);
-    issue(2);  // ns >= 4
-    wait_vmcnt<2 * (4 + AC)>();
-    __syncthreads();
-    // Each pair is read while the one before is multiplied; a stage's first pair and weights while
-    // the stage before multiplies its last.
-    Weights w = read_w(0);
-    Pair a = read_a(codes(0), scales(0), 0);
+    // Each fragment is read while the one before is multiplied; a stage's first fragment and
+    // weights while the stage before multiplies its last.
+    read_w(0, w, wsc);
+    read(codes(0), scales(0), 0, a, asc);
+    int known = 2;  // opaque, or the compiler peels the stages before it
+    asm volatile("" : "+s"(known));
+#pragma unroll 1
     for (int s = 0; s < ns; ++s) {
         const uint8_t *q = codes(s), *x = scales(s);
 #pragma unroll
-        for (int pair = 0; pair + 1 < NP; ++pair) {
-            const Pair next = read_a(q, x, pair + 1);
-            multiply(pair, a, w);
-            a = next;
+        for (int j = 0; j < 2; ++j) wsc[j] >>= 8 * g;
+        v4i na[2];
+        int nasc;
+#pragma unroll
+        for (int i = 0; i + 1 < NP; ++i) {
+            read(q, x, 32 * (i + 1), na, nasc);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(i);
+            __builtin_amdgcn_sched_barrier(0);
+            a[0] = na[0];
+            a[1] = na[1];
+            asc = nasc;
         }
-        Weights w_next = w;
-        Pair a_next = a;
+        v4i nw[2][2] = {};
+        int nwsc[2] = {};
         if (s + 1 < ns) {
-            // of stage s + 2 its last copies, all but the scales, may be under way still
-            if (s + 2 < ns) wait_vmcnt<4 + AC>();
-            else wait_vmcnt<0>();
+            // stages 0 to 2 have been waited for; of stage s + 2 the last copies, all but the
+            // scales, may be under way still
+            if (s >= known) {
+                if (s + 2 < ns) wait_vmcnt<4 + AC>();
+                else wait_vmcnt<0>();
+            }
             __syncthreads();
-            if (s + 3 < ns) issue(s + 3);
-            w_next = read_w(s + 1);
-            a_next = read_a(codes(s + 1), scales(s + 1), 0);
+            if (s + 3 < ns) mx_issue<AC>(p, c, l, s + 3);
+            read_w(s + 1, nw, nwsc);
+            read(codes(s + 1), scales(s + 1), 0, na, nasc);
         }
-        multiply(NP - 1, a, w);
-        w = w_next;
-        a = a_next;
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(NP - 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[j][0] = nw[j][0];
+            w[j][1] = nw[j][1];
+            wsc[j] = nwsc[j];
+        }
+        a[0] = na[0];
+        a[1] = na[1];
+        asc = nasc;
     }
 
+    // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
+    // that each holds eight columns in a row and stores 16 bytes.
+    constexpr int J = 2 / F;
+    uint2 out[NP][J][4];
+    // the last product's result is there after 18 wait states
+    asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-        const int row = 16 * i + r;
-        if (row >= rows) continue;
-        uint16_t *crow = p.c + (size_t)(row0 + row) * p.N;
+    for (int i = 0; i < NP; ++i) {
+        __builtin_amdgcn_sched_barrier(0);  // a few sums at a time leave the accumulators
 #pragma unroll
-        for (int j = 0; j < 4 / F; ++j) {
-            const int col = n0 + wave * (64 / F) + 16 * j + 4 * g;
-            if (col >= p.N) continue;
-            uint2 o;
-            if (SWIGLU) {
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
                 float y[4];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) y[v] = silu_times(acc[i][j][v], acc[i][j + 2][v]);
-                o = make_uint2(f2bf_pk(y[0], y[1]), f2bf_pk(y[2], y[3]));
-            } else {
-                o = make_uint2(f2h(acc[i][j][0]) | (uint32_t)f2h(acc[i][j][1]) << 16,
-                               f2h(acc[i][j][2]) | (uint32_t)f2h(acc[i][j][3]) << 16);
+                for (int v = 0; v < 4; ++v)
+                    y[v] = SWIGLU ? mx_silu_times(mx_sum(acc[i][0][4 * k + v]),
+                                                  mx_sum(acc[i][1][4 * k + v]))
+                                  : mx_sum(acc[i][j][4 * k + v]);
+                out[i][j][k] = SWIGLU ? make_uint2(f2bf_pk(y[0], y[1]), f2bf_pk(y[2], y[3]))
+                                      : make_uint2(f2h(y[0]) | (uint32_t)f2h(y[1]) << 16,
+                                                   f2h(y[2]) | (uint32_t)f2h(y[3]) << 16);
+                // rounded here, not in the blocks of the stores: half the registers
+                asm volatile("" : "+v"(out[i][j][k].x), "+v"(out[i][j][k].y));
             }
-            *reinterpret_cast<uint2 *>(crow + col) = o;
-        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) {
+        __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
+        c = mx_copies<SWIGLU>(p, nt, l);
+        mx_issue<0>(p, c, l, 0);
+        mx_issue<0>(p, c, l, 1);
+        mx_issue<0>(p, c, l, 2);
+    }
+    const int n0 = t.nblk * (kMxTile / F) + wave * (64 / F);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int row = 32 * i + r;
+        uint16_t *crow = p.c + (size_t)(t.row0 + row) * p.N;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const auto x = __builtin_amdgcn_permlane32_swap(out[i][j][k].x, out[i][j][k + 1].x, false, false);
+                const auto y = __builtin_amdgcn_permlane32_swap(out[i][j][k].y, out[i][j][k + 1].y, false, false);
+                const int col = n0 + 32 * j + 8 * (k + g);
+                if (row < t.rows && col < p.N)
+                    *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+            }
+    }
+    if (more) {
+        // The copies are older than the stores.  All but the last two fragments have whole rows,
+        // so at least that many stores were issued, unless columns past N were left out.
+        if (n0 + 64 / F <= p.N) wait_vmcnt<(NP - 2) * J * 2>();
+        else wait_vmcnt<0>();
+        __syncthreads();
     }
 }
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+__global__ __launch_bounds__(kMxTileThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void
 mxfp4_gmm_tile_kernel(MxGmmParams p) {
     constexpr int COLS = kMxTile / (SWIGLU ? 2 : 1);  // output columns of a tile
-    __shared__ int s_w[1][4];
-    __shared__ MxTile s_t;
+    __shared__ int s_w[4];
+    __shared__ MxSchedule s_s;
+    __shared__ int32_t s_route[kMxTile];
     __shared__ __align__(16) uint8_t s_data[kMxRing * kMxStageBytes];
     __shared__ __align__(16) uint8_t s_scale[2 * kMxScaleBytes];
 
-    const int NB = (p.N + COLS - 1) / COLS;
-    const MxTile tile = mx_find_tile(p, NB, blockIdx.x, s_w, &s_t);
-    const int e = __builtin_amdgcn_readfirstlane(tile.e);
-    if (e < 0) return;
-    const int row0 = __builtin_amdgcn_readfirstlane(tile.row0);
-    const int rows = __builtin_amdgcn_readfirstlane(tile.rows);
-    const int n0 = __builtin_amdgcn_readfirstlane(tile.nblk) * COLS;
-    if (rows > 192) mx_tile<SWIGLU, 8>(p, e, row0, rows, n0, s_data, s_scale);
-    else if (rows > 128) mx_tile<SWIGLU, 6>(p, e, row0, rows, n0, s_data, s_scale);
-    else if (rows > 64) mx_tile<SWIGLU, 4>(p, e, row0, rows, n0, s_data, s_scale);
-    else mx_tile<SWIGLU, 2>(p, e, row0, rows, n0, s_data, s_scale);
+    mx_schedule(p, (p.N + COLS - 1) / COLS, s_w, s_s);
+    const int total = __builtin_amdgcn_readfirstlane(s_s.total);
+    // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share
+    // weight and row blocks in its L2
+    const int per = (total + 7) / 8, step = gridDim.x >> 3;
+    const int t0 = (blockIdx.x & 7) * per, t1 = min(t0 + per, total);
+    int t = t0 + (blockIdx.x >> 3);
+    if (t >= t1) return;
+
+    const MxLds l{s_data, s_scale, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale)), s_route};
+    const int tid = threadIdx.x;
+    const uint32_t route_at =
+        __builtin_amdgcn_readfirstlane(lds_addr(s_route) + (tid >> 6) * (kWave * 4));
+    auto fetch_routes = [&](const MxTile &x) {
+        if (p.a_route) dma4(p.a_route + x.row0 + min(tid, x.rows - 1), route_at);
+    };
+    MxTile cur = mx_find_tile(s_s, t);
+    fetch_routes(cur);
+    wait_vmcnt<0>();
+    __syncthreads();
+    MxCopies c = mx_copies<SWIGLU>(p, cur, l);
+    mx_issue<0>(p, c, l, 0);
+    mx_issue<0>(p, c, l, 1);
+    mx_issue<0>(p, c, l, 2);  // at least 4 stages
+    wait_vmcnt<0>();
+    __syncthreads();
+    for (;;) {
+        t += step;
+        const bool more = t < t1;
+        const MxTile next = mx_find_tile(s_s, more ? t : t0);
+        if (more) fetch_routes(next);
+        if (cur.rows > 192) mx_tile<SWIGLU, 8>(p, cur, c, more, next, l);
+        else if (cur.rows > 128) mx_tile<SWIGLU, 6>(p, cur, c, more, next, l);
+        else if (cur.rows > 64) mx_tile<SWIGLU, 4>(p, cur, c, more, next, l);
+        else mx_tile<SWIGLU, 2>(p, cur, c, more, next, l);
+        if (!more) return;
+        cur = next;
+    }
 }
 
 template <bool SWIGLU>
-static void launch_tile(const MxGmmParams &p, hipStream_t stream) {
+static void launch_tile(const MxGmmParams &p, int cu_count, hipStream_t stream) {
     const int cols = kMxTile / (SWIGLU ? 2 : 1);
-    const long long ub = ((long long)p.R / kMxTile + (p.E < p.R ? p.E : p.R)) * ((p.N + cols - 1) / cols);
-    hipLaunchKernelGGL(mxfp4_gmm_tile_kernel<SWIGLU>, dim3((unsigned)((ub + 7) / 8 * 8)), dim3(256), 0,
-                       stream, p);
+    // at most this many tiles; one workgroup fits a CU
+    const long long most =
+        ((long long)p.R / kMxTile + (p.E < p.R ? p.E : p.R)) * ((p.N + cols - 1) / cols);
+    const long long g = most < cu_count ? most : cu_count;
+    hipLaunchKernelGGL(mxfp4_gmm_tile_kernel<SWIGLU>, dim3((unsigned)((g + 7) / 8 * 8)),
+                       dim3(kMxTileThreads), 0, stream, p);
 }
 
 hipError_t launch_mxfp4_gmm(const MxGmmParams &p, bool swiglu, int cu_count, hipStream_t stream) {
-    (void)cu_count;
     const int mean = (p.R + p.E - 1) / p.E;
     // the tiles' scale copies take 16 bytes of a row
     const bool tiles = mean > 32 && p.Kred >= 512;
-    if (swiglu) tiles ? launch_tile<true>(p, stream) : launch_stream<true>(p, stream);
-    else tiles ? launch_tile<false>(p, stream) : launch_stream<false>(p, stream);
+    if (swiglu) tiles ? launch_tile<true>(p, cu_count, stream) : launch_stream<true>(p, stream);
+    else tiles ? launch_tile<false>(p, cu_count, stream) : launch_stream<false>(p, stream);
     return hipGetLastError();
 }
 
