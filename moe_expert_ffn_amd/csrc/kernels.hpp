@@ -147,6 +147,7 @@ struct MxGmmParams {
     const int32_t *cumsum;       // [E] inclusive row prefix over experts
     uint16_t *c;                 // [R, N]
     int R, E, N, Kred, a_div;
+    uint32_t a_div_inv;          // ceil(2^32 / a_div), for a_div > 1
 };
 hipError_t launch_mxfp4_gmm(const MxGmmParams &p, bool swiglu, int cu_count, hipStream_t stream);
 

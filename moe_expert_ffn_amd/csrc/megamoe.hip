@@ -268,7 +268,10 @@ int run_mxfp4_gmm(const megamoe_dims &d, const uint8_t *a, const uint8_t *as, co
                   const int32_t *cumsum, const uint8_t *w, const uint8_t *ws, uint16_t *c,
                   bool first, hipStream_t s) {
     const MxGmmParams p{a, as, w, ws, route, cumsum, c, d.M * d.top_k, d.E,
-                        first ? d.I : d.K, first ? d.K : d.I, d.top_k};
+                        first ? d.I : d.K, first ? d.K : d.I, d.top_k,
+                        // the high product exceeds route / top_k by route * e / (top_k 2^32) with
+                        // e < top_k <= 256 and route < 2^24: by less than a step of 1 / top_k
+                        (uint32_t)(((1ull << 32) + d.top_k - 1) / d.top_k)};
     return hip_status(launch_mxfp4_gmm(p, first, cu_count_current(), s));
 }
 

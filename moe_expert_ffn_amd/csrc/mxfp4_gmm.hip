@@ -196,23 +196,24 @@ static void launch_stream(const MxGmmParams &p, hipStream_t stream) {
 // register file.  (v_mfma_scale_f32_32x32x64_f8f6f4 ran at 9.3 PFLOP/s from registers,
 // the 16x16x128 form at 5.5.)
 //
-// A stage is 128 of the reduction: 64 bytes of codes of 256 rows and 256 weight
-// rows, copied asynchronously into a ring of four stages in LDS.  The scales of
-// four stages (16 bytes a row) travel together, into two buffers.  The barrier
-// that publishes stage s + 1 lies in stage s, before its last rows are
-// multiplied: behind it the copies of stage s + 3 start (into the slot of stage
-// s - 1, which every wave has read) and the first fragments of stage s + 1 are
-// read, so that the matrix cores do not wait at a stage's start.
+// A stage is 256 of the reduction: 128 bytes of codes, a whole cache line, of 256
+// rows and 256 weight rows, copied asynchronously into one of two slots in LDS.
+// (Stages of half a line took twice the requests for the same bytes, and the L2's
+// request rate bound the kernel.)  The scales of two stages (16 bytes a row)
+// travel together, into two buffers.  The barrier between stages s and s + 1 lies
+// before the last rows of stage s are multiplied: those are in registers by then,
+// so behind it the copies of stage s + 2 start, into the slot of stage s, and the
+// first fragments of stage s + 1 are read.
 //
 // The grid is persistent.  While a tile is multiplied the workgroup looks up its
-// next one, and the first three stages of that are copied while this one's sums
-// are rounded and stored.
+// next one, and the first two stages of that are copied while this one's sums
+// are stored.
 constexpr int kMxTile = 256;                    // rows, and weight rows
-constexpr int kMxRing = 4;
-constexpr int kMxStageBytes = 2 * kMxTile * 64; // rows then weight rows
+constexpr int kMxStageBytes = 2 * kMxTile * 128; // rows then weight rows
 constexpr int kMxScaleBytes = 2 * kMxTile * 16;
 constexpr int kMxTileThreads = 256;
 constexpr int kMxE = 256;
+constexpr int kMxList = 32;
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
@@ -225,9 +226,9 @@ __device__ __forceinline__ v16f mx_mfma32(v4i w, int ws, v4i a, int as, v16f acc
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc, 4, 4, 2 * H, ws, 2 * H, as);
 }
 
-// 16-byte chunk c of a 64-byte row: the place without bank conflicts for reads of
-// one chunk index of consecutive rows by each lane group
-__device__ __forceinline__ int mx_swz(int row, int c) { return c ^ ((row >> 1) & 3); }
+// 16-byte chunk c of a 128-byte row: the place without bank conflicts for reads of
+// one chunk index of consecutive rows
+__device__ __forceinline__ int mx_swz(int row, int c) { return c ^ (row & 7); }
 
 // The tiles, numbered by expert, weight block and row block; an expert's rows are
 // split evenly over its row blocks in units of 32.
@@ -258,28 +259,24 @@ struct MxTile {
     int e, row0, rows, nblk;
 };
 __device__ __forceinline__ MxTile mx_find_tile(const MxSchedule &s, int t) {  // t < total
-    int lo = 0, hi = kMxE - 1;  // the last expert that starts at or before t and has tiles
+    int lo = 0, hi = kMxE - 1;  // the first expert that ends after t
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (s.pre[mid + 1] > t) hi = mid;
         else lo = mid + 1;
     }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int rows = __builtin_amdgcn_readfirstlane(s.rows[e]);
-    const int local = t - __builtin_amdgcn_readfirstlane(s.pre[e]);
+    const int rows = s.rows[lo], local = t - s.pre[lo];
     const int mb = (rows + kMxTile - 1) / kMxTile, m = local % mb;
     const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
     const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
-    return MxTile{e, __builtin_amdgcn_readfirstlane(s.first[e] + 32 * u0),
-                  __builtin_amdgcn_readfirstlane(min(rows, 32 * u1) - 32 * u0),
-                  __builtin_amdgcn_readfirstlane(local / mb)};
+    return MxTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, local / mb};
 }
 
 // What the copies of a tile need.
 struct MxCopies {
-    uint32_t voff_a[4], voff_w[4], soff_a, soff_w;  // per lane
+    uint32_t voff_a[8], voff_w[8], soff_a, soff_w;  // per lane
     const uint8_t *wq, *ws;                         // the expert's weights and scales
-    int ac;                                         // copies of 16 rows a wave makes, rows / 64
+    int ac;                                         // copies of 8 rows a wave makes, 2 for 64 rows
 };
 
 struct MxLds {
@@ -306,16 +303,17 @@ __device__ __forceinline__ MxCopies mx_copies(const MxGmmParams &p, const MxTile
         r = min(r, t.rows - 1);
         if (!p.a_route) return t.row0 + r;
         const int v = l.route[r];
-        return (v < 0 ? 0 : v < p.R ? v : p.R - 1) / p.a_div;
+        const uint32_t u = v < 0 ? 0 : v < p.R ? v : p.R - 1;
+        return p.a_div == 1 ? (int)u : (int)__umulhi(u, p.a_div_inv);
     };
     MxCopies c;
-    c.ac = (t.rows + 63) / 64;
+    c.ac = (t.rows + 63) / 64 * 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (wave * c.ac + i) * 16 + (lane >> 2);
-        c.voff_a[i] = (uint32_t)data_row(i < c.ac ? r : 0) * qrow + mx_swz(r, lane & 3) * 16;
-        const int n = (wave * 4 + i) * 16 + (lane >> 2);
-        c.voff_w[i] = (uint32_t)weight_row(n) * qrow + mx_swz(n, lane & 3) * 16;
+    for (int i = 0; i < 8; ++i) {
+        const int r = (wave * c.ac + i) * 8 + (lane >> 3);
+        c.voff_a[i] = (uint32_t)data_row(i < c.ac ? r : 0) * qrow + mx_swz(r, lane & 7) * 16;
+        const int n = (wave * 8 + i) * 8 + (lane >> 3);
+        c.voff_w[i] = (uint32_t)weight_row(n) * qrow + mx_swz(n, lane & 7) * 16;
     }
     c.soff_a = (uint32_t)data_row(wave * 64 + lane) * srow;
     c.soff_w = (uint32_t)weight_row(wave * 64 + lane) * srow;
@@ -324,29 +322,30 @@ __device__ __forceinline__ MxCopies mx_copies(const MxGmmParams &p, const MxTile
     return c;
 }
 
-// where the 16 scale bytes of stages 4 c .. 4 c + 3 start in a row of n; the last ones start
-// early so as to end with the row
-__device__ __forceinline__ int mx_scale_start(int c, int n) { return min(16 * c, n - 16); }
+// Where a piece of `size` bytes starts in a row of n: the last one early, so as to end with the
+// row (n is not a multiple of it where the reduction is not one of 256, for codes, or 512).
+__device__ __forceinline__ int mx_start(int piece, int size, int n) { return min(piece * size, n - size); }
 
-// The copies of stage s: at every fourth stage 2 of scales, then ac of rows and 4 of
+// The copies of stage s: at every second stage 2 of scales, then ac of rows and 8 of
 // weight rows.  AC: ac where it is known (0: not).
 template <int AC>
 __device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies &c, const MxLds &l, int s) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ac = AC ? AC : c.ac;
-    if ((s & 3) == 0) {
-        const int k = s >> 2, start = mx_scale_start(k, p.Kred / 32);
-        const uint32_t at = l.scale_at + (k & 1) * kMxScaleBytes + wave * 1024;
+    if ((s & 1) == 0) {
+        const int start = mx_start(s >> 1, 16, p.Kred / 32);
+        const uint32_t at = l.scale_at + ((s >> 1) & 1) * kMxScaleBytes + wave * 1024;
         dma16(uniform_ptr(p.a_scale + start), c.soff_a, at);
         dma16(uniform_ptr(c.ws + start), c.soff_w, at + kMxTile * 16);
     }
-    const uint32_t at = l.data_at + (s & 3) * kMxStageBytes;
-    const uint8_t *ga = uniform_ptr(p.a + (size_t)s * 64), *gw = uniform_ptr(c.wq + (size_t)s * 64);
+    const uint32_t at = l.data_at + (s & 1) * kMxStageBytes;
+    const int start = mx_start(s, 128, p.Kred / 2);
+    const uint8_t *ga = uniform_ptr(p.a + start), *gw = uniform_ptr(c.wq + start);
 #pragma unroll
-    for (int i = 0; i < (AC ? AC : 4); ++i)
+    for (int i = 0; i < (AC ? AC : 8); ++i)
         if (AC || i < ac) dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dma16(gw, c.voff_w[i], at + kMxTile * 64 + (wave * 4 + i) * 1024);
+    for (int i = 0; i < 8; ++i) dma16(gw, c.voff_w[i], at + kMxTile * 128 + (wave * 8 + i) * 1024);
 }
 
 // silu(u) * g for a result that is rounded to bf16: the reciprocal's last ulp is not corrected
@@ -363,103 +362,139 @@ __device__ __forceinline__ float mx_sum(float a) {
     return v;
 }
 
-// Multiplies tile t, of at most 32 NP rows, whose first three stages are in LDS, rounds its
-// sums, and stores them while the first stages of tile `nt` are copied.  (One body for every NP, with the rows behind
-// conditions, made the compiler move the sums between register files.)
+// Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS and whose second is
+// under way, and rounds and stores its sums while the first stages of tile `nt` are copied.
+// (One body for every NP, with the rows behind conditions, made the compiler move the sums
+// between register files.)
 template <bool SWIGLU, int NP>
 __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies &c,
                                         bool more, const MxTile &nt, const MxLds &l) {
-    constexpr int F = SWIGLU ? 2 : 1, AC = NP / 2;
+    constexpr int F = SWIGLU ? 2 : 1;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ns = p.Kred / 128;
+    const int ns = (p.Kred + 255) / 256;
+    const bool half = p.Kred % 256 != 0;  // of the last stage's row pieces the second halves alone
 
     const int r = lane & 31, g = lane >> 5;
-    const int frag_off[2] = {r * 64 + mx_swz(r, g) * 16, r * 64 + mx_swz(r, 2 + g) * 16};
-    // LDS addresses of stage s, tile row 0
-    auto codes = [&](int s) { return l.data + (s & 3) * kMxStageBytes; };
-    auto scales = [&](int s) {
-        const int k = s >> 2;
-        return l.scale + (k & 1) * kMxScaleBytes + r * 16 + 4 * s - mx_scale_start(k, p.Kred / 32);
-    };
-    // 32 rows of a stage: two fragments, and the rows' four scale bytes
-    auto read = [&](const uint8_t *q, const uint8_t *x, int row, v4i (&f)[2], int &sc) {
+    int frag_off[4];  // lane's place in 32 rows of a stage, 64 of the reduction each
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            f[h] = *reinterpret_cast<const v4i *>(q + row * 64 + frag_off[h]);
-        sc = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
+    for (int h = 0; h < 4; ++h) frag_off[h] = r * 128 + mx_swz(r, 2 * h + g) * 16;
+    // LDS addresses of stage s, tile row 0
+    auto codes = [&](int s) { return l.data + (s & 1) * kMxStageBytes; };
+    auto scales = [&](int s) {
+        return l.scale + ((s >> 1) & 1) * kMxScaleBytes + r * 16 + mx_start(s, 8, p.Kred / 32) -
+               mx_start(s >> 1, 16, p.Kred / 32);
     };
-    auto read_w = [&](int s, v4i (&f)[2][2], int (&sc)[2]) {
+    // 32 rows of a stage: four fragments, and the rows' eight scale bytes
+    auto read = [&](const uint8_t *q, const uint8_t *x, int row, v4i (&f)[4], int (&sc)[2]) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            f[h] = *reinterpret_cast<const v4i *>(q + row * 128 + frag_off[h]);
+        sc[0] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
+        sc[1] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16 + 4);
+    };
+    auto read_w = [&](int s, v4i (&f)[2][4], int (&sc)[2][2]) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             read(codes(s), scales(s), kMxTile + wave * 64 + 32 * j, f[j], sc[j]);
     };
     v16f acc[NP][2] = {};
-    v4i w[2][2], a[2];  // weights of the stage, rows of the fragment that is multiplied
-    int wsc[2], asc;
-    auto multiply = [&](int i) {
-        const int as = asc >> (8 * g);  // the lane's blocks are g and 2 + g
+    v4i w[2][4], a[2][4];  // weights of the stage, rows of the two fragments that are multiplied
+    int wsc[2][2], asc[2][2];
+    auto read_a = [&](const uint8_t *q, const uint8_t *x, int pair, v4i (&f)[2][4], int (&sc)[2][2]) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma32<0>(w[j][0], wsc[j], a[0], as, acc[i][j]);
+        for (int i = 0; i < 2; ++i) read(q, x, 64 * pair + 32 * i, f[i], sc[i]);
+    };
+    // Two row fragments by two weight fragments: four sums that take turns, so that no product
+    // waits for the one before it.  (With two, the loop ran at half the rate.)
+    auto multiply = [&](int pair, int first_half) {  // first_half: 0 or -1
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mx_mfma32<1>(w[j][1], wsc[j], a[1], as, acc[i][j]);
+        for (int i = 0; i < 2; ++i) {
+            asc[i][0] >>= 8 * g;  // the lane's blocks are g and 2 + g of each half
+            asc[i][1] >>= 8 * g;
+            // Codes of 0 where the first half has been multiplied before.  (A NaN scale makes a
+            // NaN of them, but where it did so before.)
+            a[i][0] &= first_half;
+            a[i][1] &= first_half;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v16f &d = acc[2 * pair + i][j];
+                    d = h & 1 ? mx_mfma32<1>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d)
+                              : mx_mfma32<0>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d);
+                }
         // the sums are wanted here: without this the compiler puts a stage's products together
         // behind its barrier and copies, where the reads no longer overlap them
 #pragma unroll
-        for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[i][j]));
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[2 * pair + i][j]));
     };
 
-    // Each fragment is read while the one before is multiplied; a stage's first fragment and
+    // Each pair of fragments is read while the one before is multiplied; a stage's first pair and
     // weights while the stage before multiplies its last.
     read_w(0, w, wsc);
-    read(codes(0), scales(0), 0, a, asc);
-    int known = 2;  // opaque, or the compiler peels the stages before it
-    asm volatile("" : "+s"(known));
+    read_a(codes(0), scales(0), 0, a, asc);
 #pragma unroll 1
     for (int s = 0; s < ns; ++s) {
         const uint8_t *q = codes(s), *x = scales(s);
+        const int first_half = half && s + 1 == ns ? 0 : -1;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) wsc[j] >>= 8 * g;
-        v4i na[2];
-        int nasc;
-#pragma unroll
-        for (int i = 0; i + 1 < NP; ++i) {
-            read(q, x, 32 * (i + 1), na, nasc);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(i);
-            __builtin_amdgcn_sched_barrier(0);
-            a[0] = na[0];
-            a[1] = na[1];
-            asc = nasc;
+        for (int j = 0; j < 2; ++j) {
+            wsc[j][0] >>= 8 * g;
+            wsc[j][1] >>= 8 * g;
         }
-        v4i nw[2][2] = {};
-        int nwsc[2] = {};
-        if (s + 1 < ns) {
-            // stages 0 to 2 have been waited for; of stage s + 2 the last copies, all but the
-            // scales, may be under way still
-            if (s >= known) {
-                if (s + 2 < ns) wait_vmcnt<4 + AC>();
-                else wait_vmcnt<0>();
+        v4i na[2][4];
+        int nasc[2][2];
+        auto shift = [&]() {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) a[i][h] = na[i][h];
+                asc[i][0] = nasc[i][0];
+                asc[i][1] = nasc[i][1];
             }
+        };
+#pragma unroll
+        for (int pair = 0; pair + 1 < NP / 2; ++pair) {
+            read_a(q, x, pair + 1, na, nasc);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(pair, first_half);
+            __builtin_amdgcn_sched_barrier(0);
+            shift();
+        }
+        v4i nw[2][4] = {};
+        int nwsc[2][2] = {};
+        if (s + 1 < ns) {
+            wait_vmcnt<0>();  // stage s + 1
             __syncthreads();
-            if (s + 3 < ns) mx_issue<AC>(p, c, l, s + 3);
+            if (s + 2 < ns) mx_issue<NP>(p, c, l, s + 2);
             read_w(s + 1, nw, nwsc);
-            read(codes(s + 1), scales(s + 1), 0, na, nasc);
+            read_a(codes(s + 1), scales(s + 1), 0, na, nasc);
         }
         __builtin_amdgcn_sched_barrier(0);
-        multiply(NP - 1);
+        multiply(NP / 2 - 1, first_half);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            w[j][0] = nw[j][0];
-            w[j][1] = nw[j][1];
-            wsc[j] = nwsc[j];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[j][h] = nw[j][h];
+            wsc[j][0] = nwsc[j][0];
+            wsc[j][1] = nwsc[j][1];
         }
-        a[0] = na[0];
-        a[1] = na[1];
-        asc = nasc;
+        shift();
     }
 
+    if (more) {
+        __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
+        c = mx_copies<SWIGLU>(p, nt, l);
+        mx_issue<0>(p, c, l, 0);
+        mx_issue<0>(p, c, l, 1);
+    }
     // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
     // that each holds eight columns in a row and stores 16 bytes.
     constexpr int J = 2 / F;
@@ -487,13 +522,6 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (more) {
-        __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
-        c = mx_copies<SWIGLU>(p, nt, l);
-        mx_issue<0>(p, c, l, 0);
-        mx_issue<0>(p, c, l, 1);
-        mx_issue<0>(p, c, l, 2);
-    }
     const int n0 = t.nblk * (kMxTile / F) + wave * (64 / F);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -511,10 +539,11 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             }
     }
     if (more) {
-        // The copies are older than the stores.  All but the last two fragments have whole rows,
-        // so at least that many stores were issued, unless columns past N were left out.
-        if (n0 + 64 / F <= p.N) wait_vmcnt<(NP - 2) * J * 2>();
-        else wait_vmcnt<0>();
+        // The first stage's copies are older than the second's, 10 at least, and than the stores:
+        // all but the last two fragments have whole rows, so at least that many were issued,
+        // unless columns past N were left out.
+        if (n0 + 64 / F <= p.N) wait_vmcnt<10 + (NP - 2) * J * 2>();
+        else wait_vmcnt<10>();
         __syncthreads();
     }
 }
@@ -525,8 +554,9 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     constexpr int COLS = kMxTile / (SWIGLU ? 2 : 1);  // output columns of a tile
     __shared__ int s_w[4];
     __shared__ MxSchedule s_s;
+    __shared__ MxTile s_t[kMxList];
     __shared__ int32_t s_route[kMxTile];
-    __shared__ __align__(16) uint8_t s_data[kMxRing * kMxStageBytes];
+    __shared__ __align__(16) uint8_t s_data[2 * kMxStageBytes];
     __shared__ __align__(16) uint8_t s_scale[2 * kMxScaleBytes];
 
     mx_schedule(p, (p.N + COLS - 1) / COLS, s_w, s_s);
@@ -534,32 +564,44 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share
     // weight and row blocks in its L2
     const int per = (total + 7) / 8, step = gridDim.x >> 3;
-    const int t0 = (blockIdx.x & 7) * per, t1 = min(t0 + per, total);
-    int t = t0 + (blockIdx.x >> 3);
-    if (t >= t1) return;
+    const int t0 = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int t1 = min((int)(blockIdx.x & 7) * per + per, total);
+    const int n = t0 < t1 ? (t1 - t0 + step - 1) / step : 0;  // tiles of this workgroup
+    if (n == 0) return;
 
     const MxLds l{s_data, s_scale, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
-                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale)), s_route};
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale)),
+                  s_route};
     const int tid = threadIdx.x;
     const uint32_t route_at =
         __builtin_amdgcn_readfirstlane(lds_addr(s_route) + (tid >> 6) * (kWave * 4));
     auto fetch_routes = [&](const MxTile &x) {
         if (p.a_route) dma4(p.a_route + x.row0 + min(tid, x.rows - 1), route_at);
     };
-    MxTile cur = mx_find_tile(s_s, t);
+    // its tiles are looked up kMxList at a time, a lane each
+    auto look_up = [&](int k) {
+        if (tid < kMxList && k + tid < n) s_t[tid] = mx_find_tile(s_s, t0 + (k + tid) * step);
+        __syncthreads();
+    };
+    auto tile = [&](int k) {
+        const MxTile &x = s_t[k % kMxList];
+        return MxTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.row0),
+                      __builtin_amdgcn_readfirstlane(x.rows), __builtin_amdgcn_readfirstlane(x.nblk)};
+    };
+    look_up(0);
+    MxTile cur = tile(0);
     fetch_routes(cur);
     wait_vmcnt<0>();
     __syncthreads();
     MxCopies c = mx_copies<SWIGLU>(p, cur, l);
     mx_issue<0>(p, c, l, 0);
-    mx_issue<0>(p, c, l, 1);
-    mx_issue<0>(p, c, l, 2);  // at least 4 stages
-    wait_vmcnt<0>();
+    mx_issue<0>(p, c, l, 1);  // at least 2 stages
+    wait_vmcnt<10>();
     __syncthreads();
-    for (;;) {
-        t += step;
-        const bool more = t < t1;
-        const MxTile next = mx_find_tile(s_s, more ? t : t0);
+    for (int k = 1;; ++k) {
+        const bool more = k < n;
+        if (more && k % kMxList == 0) look_up(k);  // the last tiles of the list have been read
+        const MxTile next = more ? tile(k) : cur;
         if (more) fetch_routes(next);
         if (cur.rows > 192) mx_tile<SWIGLU, 8>(p, cur, c, more, next, l);
         else if (cur.rows > 128) mx_tile<SWIGLU, 6>(p, cur, c, more, next, l);
