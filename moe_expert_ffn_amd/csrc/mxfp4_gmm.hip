@@ -15,207 +15,38 @@
 namespace megamoe {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// 16 x 16 x 128 with weights as the first operand: lane l holds output row l & 15
-// and the columns 4 (l >> 4) + 0..3.  Of either operand lane l has row l & 15, the
-// codes of block l >> 4 and, in the low byte, their scale.
-__device__ __forceinline__ v4f mx_mfma(v4i w, int ws, v4i a, int as, v4f acc) {
-    const v8i w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0}, a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, acc, 4, 4, 0, ws, 0, as);
-}
-
-// fp32 -> the output element, round to nearest even
-template <bool SWIGLU>
-__device__ __forceinline__ uint16_t mx_out(float v) {
-    return SWIGLU ? (uint16_t)(f2bf_pk(v, 0.0f) & 0xffffu) : f2h(v);
-}
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 // first row and row count of expert e's group, within [0, R]
 __device__ __forceinline__ int mx_row_end(const MxGmmParams &p, int e) {
     const int v = e >= 0 ? p.cumsum[e] : 0;
     return v < 0 ? 0 : v > p.R ? p.R : v;
 }
-__device__ __forceinline__ size_t mx_a_row(const MxGmmParams &p, int d) {
-    if (!p.a_route) return d;
-    const int r = p.a_route[d];
-    return (r < 0 ? 0 : r < p.R ? r : p.R - 1) / p.a_div;
-}
 
-// ---------------------------------------------------------------------------
-// Few rows per expert: the product streams weights.  One workgroup per expert
-// with rows and 16 output columns; its waves split the reduction, each reading
-// weights and rows straight into fragments, and the partial sums are added in
-// wave order.
-constexpr int kMxWaves = 8;
-constexpr int kMxThreads = kMxWaves * kWave;
-
-template <bool SWIGLU, int RB>
-__global__ __launch_bounds__(kMxThreads) void mxfp4_gmm_stream_kernel(MxGmmParams p) {
-    constexpr int F = SWIGLU ? 2 : 1;  // weight fragments of a column group
-    constexpr int U = RB > 2 ? 2 : 4;  // K slices a wave has in flight
-    __shared__ int s_e;
-    __shared__ v4f s_part[kMxWaves][RB * F][kWave];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid >> 6;
-
-    if (tid < kWave) {  // the expert of this workgroup: the blockIdx.y-th with rows
-        int any[4], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int e = tid * 4 + j;
-            any[j] = e < p.E && mx_row_end(p, e) > mx_row_end(p, e - 1);
-            sum += any[j];
-        }
-        int run = wave_inclusive_scan(sum) - sum;
-        if (tid == 0) s_e = -1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (any[j] && run == (int)blockIdx.y) s_e = tid * 4 + j;
-            run += any[j];
-        }
-    }
-    __syncthreads();
-    const int e = s_e;
-    if (e < 0) return;
-    const int row0 = mx_row_end(p, e - 1), rows = mx_row_end(p, e) - row0;
-
-    const int ns = p.Kred / 128, n0 = blockIdx.x * 16;
-    const int s0 = wave * ns / kMxWaves, s1 = (wave + 1) * ns / kMxWaves;
-    const size_t qrow = p.Kred / 2, srow = p.Kred / 32;
-    const int r = lane & 15, g = lane >> 4;
-    const uint8_t *wq[F], *wsc[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-        const size_t n = (size_t)e * p.N * F + f * p.N + n0 + r;
-        wq[f] = p.w + n * qrow + g * 16;
-        wsc[f] = p.w_scale + n * srow + g;
-    }
-    const v4i zero = {0, 0, 0, 0};
-
-    for (int r0 = 0; r0 < rows; r0 += 16 * RB) {
-        const uint8_t *aq[RB], *asc[RB];
-        bool in[RB];
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            in[b] = r0 + 16 * b + r < rows;
-            const size_t d = mx_a_row(p, row0 + (in[b] ? r0 + 16 * b + r : r0));
-            aq[b] = p.a + d * qrow + g * 16;
-            asc[b] = p.a_scale + d * srow + g;
-        }
-        v4f acc[RB][F] = {};
-        v4i fw[U][F], fa[U][RB];
-        int cw[U][F], ca[U][RB];
-        auto load = [&](int s) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    fw[i][f] = zero;
-                    cw[i][f] = 0;
-                    if (s + i < s1) {
-                        fw[i][f] = __builtin_nontemporal_load(
-                            reinterpret_cast<const v4i *>(wq[f] + (size_t)(s + i) * 64));
-                        cw[i][f] = wsc[f][(s + i) * 4];
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    fa[i][b] = zero;
-                    ca[i][b] = 0;
-                    if (s + i < s1 && in[b]) {
-                        fa[i][b] = *reinterpret_cast<const v4i *>(aq[b] + (size_t)(s + i) * 64);
-                        ca[i][b] = asc[b][(s + i) * 4];
-                    }
-                }
-            }
-        };
-        load(s0);
-        for (int s = s0; s < s1; s += U) {
-            v4i bw[U][F], ba[U][RB];
-            int sw[U][F], sa[U][RB];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    bw[i][f] = fw[i][f];
-                    sw[i][f] = cw[i][f];
-                }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    ba[i][b] = fa[i][b];
-                    sa[i][b] = ca[i][b];
-                }
-            }
-            if (s + U < s1) load(s + U);
-#pragma unroll
-            for (int i = 0; i < U; ++i)
-#pragma unroll
-                for (int b = 0; b < RB; ++b)
-#pragma unroll
-                    for (int f = 0; f < F; ++f)
-                        if (s + i < s1) acc[b][f] = mx_mfma(bw[i][f], sw[i][f], ba[i][b], sa[i][b], acc[b][f]);
-        }
-        __syncthreads();  // the last pass's sums have been read
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int f = 0; f < F; ++f) s_part[wave][b * F + f][lane] = acc[b][f];
-        __syncthreads();
-        for (int i = tid; i < RB * 256; i += kMxThreads) {  // row i / 16, column i % 16
-            const int row = i >> 4, col = i & 15;
-            if (r0 + row >= rows) break;
-            const int at = (row & 15) + 16 * (col >> 2), b = row >> 4;
-            float sum[F];
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-                sum[f] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kMxWaves; ++w)
-                    sum[f] += reinterpret_cast<const float *>(&s_part[w][b * F + f][at])[col & 3];
-            }
-            const float v = SWIGLU ? silu_times(sum[0], sum[F - 1]) : sum[0];
-            p.c[(size_t)(row0 + r0 + row) * p.N + n0 + col] = mx_out<SWIGLU>(v);
-        }
-    }
-}
-
-template <bool SWIGLU>
-static void launch_stream(const MxGmmParams &p, hipStream_t stream) {
-    const dim3 grid(p.N / 16, p.E < p.R ? p.E : p.R), block(kMxThreads);
-    const int mean = (p.R + p.E - 1) / p.E;
-    if (mean <= 8) hipLaunchKernelGGL((mxfp4_gmm_stream_kernel<SWIGLU, 1>), grid, block, 0, stream, p);
-    else if (mean <= 24) hipLaunchKernelGGL((mxfp4_gmm_stream_kernel<SWIGLU, 2>), grid, block, 0, stream, p);
-    else hipLaunchKernelGGL((mxfp4_gmm_stream_kernel<SWIGLU, 4>), grid, block, 0, stream, p);
-}
-
-// ---------------------------------------------------------------------------
-// Many rows per expert: tiles of 256 rows by 256 weight rows on the matrix cores.
-// Four waves, one to a SIMD, each multiply all rows of the tile by 64 of its
-// weight rows, so that the time of a tile follows its live rows in steps of 64 and
-// no wave idles in a ragged one; 8 x 2 fragments of 32 x 32 sums fill half of the
-// register file.  (v_mfma_scale_f32_32x32x64_f8f6f4 ran at 9.3 PFLOP/s from registers,
-// the 16x16x128 form at 5.5.)
+// Both kernels below work through tiles of AR rows by WR weight rows, four waves to a
+// tile, each multiplying all of its rows by a quarter of its weight rows with
+// v_mfma_scale_f32_32x32x64_f8f6f4.  (From registers that ran at 9.3 PFLOP/s on constant
+// operands and 6.5 on random ones, where the card throttles; the 16x16x128 form at 5.5.)
 //
-// A stage is 256 of the reduction: 128 bytes of codes, a whole cache line, of 256
-// rows and 256 weight rows, copied asynchronously into one of two slots in LDS.
-// (Stages of half a line took twice the requests for the same bytes, and the L2's
-// request rate bound the kernel.)  The scales of two stages (16 bytes a row)
-// travel together, into two buffers.  The barrier between stages s and s + 1 lies
-// before the last rows of stage s are multiplied: those are in registers by then,
-// so behind it the copies of stage s + 2 start, into the slot of stage s, and the
-// first fragments of stage s + 1 are read.
-//
-// The grid is persistent.  While a tile is multiplied the workgroup looks up its
-// next one, and the first two stages of that are copied while this one's sums
-// are stored.
-constexpr int kMxTile = 256;                    // rows, and weight rows
-constexpr int kMxStageBytes = 2 * kMxTile * 128; // rows then weight rows
-constexpr int kMxScaleBytes = 2 * kMxTile * 16;
-constexpr int kMxTileThreads = 256;
+// A stage is 256 of the reduction: 128 bytes of codes, a whole cache line, of every
+// row, copied asynchronously into LDS.  (Stages of half a line took twice the
+// requests for the same bytes.)  The scales of two stages, 16 bytes a row, travel
+// together.  Where the reduction ends inside a stage, the last piece of a row starts
+// early so as to end with it, and what it holds a second time is multiplied as 0.
+constexpr int kMxThreads = 256;
 constexpr int kMxE = 256;
-constexpr int kMxList = 32;
 
-typedef float v16f __attribute__((ext_vector_type(16)));
+template <bool SWIGLU_, int AR_, int WR_>
+struct MxGeom {
+    static constexpr bool SWIGLU = SWIGLU_;
+    static constexpr int AR = AR_, WR = WR_;
+    static constexpr int COLS = SWIGLU ? WR / 2 : WR;  // output columns
+    static constexpr int WRW = WR / 4;                 // weight rows of a wave
+    static constexpr int STAGE = (AR + WR) * 128;      // bytes of a stage: rows, then weight rows
+    static constexpr int SCALE = (AR + WR) * 16;       // bytes of two stages' scales
+    static constexpr int AC = AR / 32, WC = WR / 32;   // copies of 8 rows a wave makes, at most
+    static constexpr int SC = (AR + WR + 255) / 256;   // copies of 64 rows' scales
+};
 
 // 32 x 32 x 64 with weights as the first operand: lane l holds output row l & 31 and
 // the columns 8 q + 4 (l >> 5) + 0..3, q = 0..3.  Of either operand lane l has row
@@ -237,11 +68,12 @@ struct MxSchedule {
     int first[kMxE], rows[kMxE];
     int total;
 };
-__device__ __forceinline__ void mx_schedule(const MxGmmParams &p, int NB, int *s_w, MxSchedule &s) {
+template <typename G>
+__device__ __forceinline__ void mx_schedule(const MxGmmParams &p, int *s_w, MxSchedule &s) {
     const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
     const int first = e < p.E ? mx_row_end(p, e - 1) : 0;
     const int rows = e < p.E ? max(0, mx_row_end(p, e) - first) : 0;
-    const int tiles = (rows + kMxTile - 1) / kMxTile * NB;
+    const int tiles = (rows + G::AR - 1) / G::AR * ((p.N + G::COLS - 1) / G::COLS);
     const int incl = wave_inclusive_scan(tiles);
     if (lane == kWave - 1) s_w[wave] = incl;
     __syncthreads();
@@ -258,6 +90,7 @@ __device__ __forceinline__ void mx_schedule(const MxGmmParams &p, int NB, int *s
 struct MxTile {
     int e, row0, rows, nblk;
 };
+template <typename G>
 __device__ __forceinline__ MxTile mx_find_tile(const MxSchedule &s, int t) {  // t < total
     int lo = 0, hi = kMxE - 1;  // the first expert that ends after t
     while (lo < hi) {
@@ -266,93 +99,175 @@ __device__ __forceinline__ MxTile mx_find_tile(const MxSchedule &s, int t) {  //
         else lo = mid + 1;
     }
     const int rows = s.rows[lo], local = t - s.pre[lo];
-    const int mb = (rows + kMxTile - 1) / kMxTile, m = local % mb;
+    const int mb = (rows + G::AR - 1) / G::AR, m = local % mb;
     const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
     const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
     return MxTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, local / mb};
 }
-
-// What the copies of a tile need.
-struct MxCopies {
-    uint32_t voff_a[8], voff_w[8], soff_a, soff_w;  // per lane
-    const uint8_t *wq, *ws;                         // the expert's weights and scales
-    int ac;                                         // copies of 8 rows a wave makes, 2 for 64 rows
-};
+__device__ __forceinline__ MxTile mx_uniform(const MxTile &x) {
+    return MxTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.row0),
+                  __builtin_amdgcn_readfirstlane(x.rows), __builtin_amdgcn_readfirstlane(x.nblk)};
+}
 
 struct MxLds {
     uint8_t *data, *scale;
     uint32_t data_at, scale_at;  // their LDS addresses
-    int32_t *route;              // [256] A rows of the next tile, as sorted routes
+    int32_t *route;              // [AR] rows of the tile that is copied next, as sorted routes
 };
 
-template <bool SWIGLU>
-__device__ __forceinline__ MxCopies mx_copies(const MxGmmParams &p, const MxTile &t, const MxLds &l) {
-    constexpr int F = SWIGLU ? 2 : 1;
+// row r of tile t -> row of A; rows past the group are its last one
+__device__ __forceinline__ uint32_t mx_data_row(const MxGmmParams &p, const MxTile &t, const MxLds &l,
+                                                int r) {
+    r = min(r, t.rows - 1);
+    if (!p.a_route) return t.row0 + r;
+    const int v = l.route[r];
+    const uint32_t u = v < 0 ? 0 : v < p.R ? v : p.R - 1;
+    return p.a_div == 1 ? u : __umulhi(u, p.a_div_inv);
+}
+// weight row r of tile t -> weight row of the expert: with SwiGLU a wave's are as many silu
+// columns and the gate columns that go with them
+template <typename G>
+__device__ __forceinline__ uint32_t mx_weight_row(const MxGmmParams &p, const MxTile &t, int r) {
+    const int w = r / G::WRW, c = r % G::WRW;
+    constexpr int H = G::WRW / 2;
+    const int col = t.nblk * G::COLS + (G::SWIGLU ? H * w + c % H : r);
+    return min(col, p.N - 1) + (G::SWIGLU && c >= H ? p.N : 0);
+}
+
+// What the copies of a tile need.
+template <typename G>
+struct MxCopies {
+    uint32_t voff_a[G::AC], voff_w[G::WC], soff[G::SC];  // per lane
+    const uint8_t *wq, *ws;                              // the expert's weights and scales
+    int ac;                                              // copies of 8 rows a wave makes
+};
+// Copy i of scales is of 64 weight rows or, past them, of 64 rows (the last ones again where the
+// copies are more).
+template <typename G>
+__device__ __forceinline__ int mx_scale_copy(int i, int wave) {
+    return min(4 * i + wave, (G::AR + G::WR) / 64 - 1);
+}
+// unit: rows go to the waves 32 * unit at a time
+template <typename G>
+__device__ __forceinline__ MxCopies<G> mx_copies(const MxGmmParams &p, const MxTile &t, const MxLds &l,
+                                                 int unit) {
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t qrow = p.Kred / 2, srow = p.Kred / 32;
-    const int n0 = t.nblk * (kMxTile / F);
-    // tile weight row r -> weight row of the expert: wave w's 64 are, with SwiGLU, 32 silu
-    // columns and the 32 gate columns that go with them
-    auto weight_row = [&](int r) {
-        const int w = r >> 6, c = r & 63;
-        const int col = SWIGLU ? n0 + 32 * w + (c & 31) : n0 + r;
-        return min(col, p.N - 1) + (SWIGLU && c >= 32 ? p.N : 0);
+    constexpr int F = G::SWIGLU ? 2 : 1;
+    MxCopies<G> c;
+    c.ac = (t.rows + 32 * unit - 1) / (32 * unit) * unit;
+    // a row of 64 bytes: its piece starts 64 bytes early, and what lies there is not its own
+    auto place = [&](int r) {
+        const int chunk = mx_swz(r, lane & 7);
+        return chunk * 16 + (qrow < 128 && chunk < 4 ? 64 : 0);
     };
-    auto data_row = [&](int r) {
-        r = min(r, t.rows - 1);
-        if (!p.a_route) return t.row0 + r;
-        const int v = l.route[r];
-        const uint32_t u = v < 0 ? 0 : v < p.R ? v : p.R - 1;
-        return p.a_div == 1 ? (int)u : (int)__umulhi(u, p.a_div_inv);
-    };
-    MxCopies c;
-    c.ac = (t.rows + 63) / 64 * 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < G::AC; ++i) {
         const int r = (wave * c.ac + i) * 8 + (lane >> 3);
-        c.voff_a[i] = (uint32_t)data_row(i < c.ac ? r : 0) * qrow + mx_swz(r, lane & 7) * 16;
-        const int n = (wave * 8 + i) * 8 + (lane >> 3);
-        c.voff_w[i] = (uint32_t)weight_row(n) * qrow + mx_swz(n, lane & 7) * 16;
+        c.voff_a[i] = mx_data_row(p, t, l, i < c.ac ? r : 0) * qrow + place(r);
     }
-    c.soff_a = (uint32_t)data_row(wave * 64 + lane) * srow;
-    c.soff_w = (uint32_t)weight_row(wave * 64 + lane) * srow;
+#pragma unroll
+    for (int i = 0; i < G::WC; ++i) {
+        const int r = (wave * G::WC + i) * 8 + (lane >> 3);
+        c.voff_w[i] = mx_weight_row<G>(p, t, r) * qrow + place(r);
+    }
+#pragma unroll
+    for (int i = 0; i < G::SC; ++i) {
+        const int k = mx_scale_copy<G>(i, wave);
+        c.soff[i] = srow * (k < G::WR / 64 ? mx_weight_row<G>(p, t, 64 * k + lane)
+                                           : mx_data_row(p, t, l, 64 * k - G::WR + lane));
+    }
     c.wq = uniform_ptr(p.w + (size_t)t.e * p.N * F * qrow);
     c.ws = uniform_ptr(p.w_scale + (size_t)t.e * p.N * F * srow);
     return c;
 }
 
-// Where a piece of `size` bytes starts in a row of n: the last one early, so as to end with the
-// row (n is not a multiple of it where the reduction is not one of 256, for codes, or 512).
+// Where a piece of `size` bytes starts in a row of n: the last one early, so as to end with the row.
 __device__ __forceinline__ int mx_start(int piece, int size, int n) { return min(piece * size, n - size); }
+// the same for the 16 bytes of two stages' scales, the row's start where it is shorter
+__device__ __forceinline__ int mx_scale_start(int s, int n) { return max(0, mx_start(s >> 1, 16, n)); }
 
-// The copies of stage s: at every second stage 2 of scales, then ac of rows and 8 of
-// weight rows.  AC: ac where it is known (0: not).
-template <int AC>
-__device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies &c, const MxLds &l, int s) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ac = AC ? AC : c.ac;
-    if ((s & 1) == 0) {
-        const int start = mx_start(s >> 1, 16, p.Kred / 32);
-        const uint32_t at = l.scale_at + ((s >> 1) & 1) * kMxScaleBytes + wave * 1024;
-        dma16(uniform_ptr(p.a_scale + start), c.soff_a, at);
-        dma16(uniform_ptr(c.ws + start), c.soff_w, at + kMxTile * 16);
+// Scales of rows under 16 bytes are all of two stages; a 16-byte copy of the last one would
+// pass the buffer's end, so they are read and written word by word, with the first stage.
+template <typename G>
+__device__ __forceinline__ void mx_short_scales(const MxGmmParams &p, const MxTile &t,
+                                                const MxCopies<G> &c, const MxLds &l) {
+    const int srow = p.Kred / 32;
+    if (srow >= 16) return;
+    for (int r = threadIdx.x; r < G::AR + G::WR; r += kMxThreads) {
+        const uint8_t *q = r < G::AR ? p.a_scale + (size_t)mx_data_row(p, t, l, r) * srow
+                                     : c.ws + (size_t)mx_weight_row<G>(p, t, r - G::AR) * srow;
+        for (int k = 0; k < srow; k += 4)
+            *reinterpret_cast<uint32_t *>(l.scale + r * 16 + k) = *reinterpret_cast<const uint32_t *>(q + k);
     }
-    const uint32_t at = l.data_at + (s & 1) * kMxStageBytes;
+}
+
+// The copies of stage s into slot `slot`: at every second stage SC of scales, then ac of rows and WC
+// of weight rows.  AC: ac where it is known (0: not).
+template <typename G, int AC>
+__device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies<G> &c, const MxLds &l, int s,
+                                         int slot) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ac = AC ? AC : c.ac, srow = p.Kred / 32;
+    if ((s & 1) == 0 && srow >= 16) {
+        const int start = mx_scale_start(s, srow);
+        const uint32_t at = l.scale_at + ((s >> 1) & 1) * G::SCALE;
+#pragma unroll
+        for (int i = 0; i < G::SC; ++i) {
+            const int k = mx_scale_copy<G>(i, wave);
+            const bool w = k < G::WR / 64;
+            dma16(uniform_ptr((w ? c.ws : p.a_scale) + start), c.soff[i],
+                  at + (w ? G::AR + 64 * k : 64 * k - G::WR) * 16);
+        }
+    }
+    const uint32_t at = l.data_at + slot * G::STAGE;
     const int start = mx_start(s, 128, p.Kred / 2);
     const uint8_t *ga = uniform_ptr(p.a + start), *gw = uniform_ptr(c.wq + start);
 #pragma unroll
-    for (int i = 0; i < (AC ? AC : 8); ++i)
+    for (int i = 0; i < (AC ? AC : G::AC); ++i)
         if (AC || i < ac) dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dma16(gw, c.voff_w[i], at + kMxTile * 128 + (wave * 8 + i) * 1024);
+    for (int i = 0; i < G::WC; ++i) dma16(gw, c.voff_w[i], at + G::AR * 128 + (wave * G::WC + i) * 1024);
 }
+
+// Reads of a stage in LDS: 32 rows from `row`, four fragments of 64 of the reduction and eight scale bytes.
+template <typename G>
+struct MxStage {
+    const uint8_t *q, *x;
+    __device__ __forceinline__ MxStage(const MxGmmParams &p, const MxLds &l, int s, int slot) {
+        const int r = threadIdx.x & 31, srow = p.Kred / 32;
+        q = l.data + slot * G::STAGE + r * 128;
+        x = l.scale + ((s >> 1) & 1) * G::SCALE + r * 16 + mx_start(s, 8, srow) - mx_scale_start(s, srow);
+    }
+    __device__ __forceinline__ void read(int row, const int (&place)[4], v4i (&f)[4], int (&sc)[2]) const {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) f[h] = *reinterpret_cast<const v4i *>(q + row * 128 + place[h]);
+        sc[0] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
+        sc[1] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16 + 4);
+    }
+};
 
 // silu(u) * g for a result that is rounded to bf16: the reciprocal's last ulp is not corrected
 __device__ __forceinline__ float mx_silu_times(float u, float g) {
     const float d = __builtin_amdgcn_exp2f(u * -1.4426950408889634f) + 1.0f;
     return u * __builtin_amdgcn_rcpf(d) * g;
 }
+
+// ---------------------------------------------------------------------------
+// Many rows per expert: tiles of 256 by 256, one wave to a SIMD, so that the time of a
+// tile follows its live rows in steps of 64 and no wave idles in a ragged one; 8 x 2
+// fragments of 32 x 32 sums fill half of the register file.
+//
+// The stages alternate between two slots.  The barrier between stages s and s + 1 lies
+// before the last rows of stage s are multiplied: those are in registers by then,
+// so behind it the copies of stage s + 2 start, into the slot of stage s, and the
+// first fragments of stage s + 1 are read.
+//
+// The grid is persistent.  While a tile is multiplied the workgroup looks up its
+// next one, and the first two stages of that are copied while this one's sums
+// are rounded and stored.
+constexpr int kMxList = 32;
 
 // One sum out of the accumulation registers.  (Left to the compiler, all 256 are copied
 // at once and other values spill.)
@@ -366,9 +281,10 @@ __device__ __forceinline__ float mx_sum(float a) {
 // under way, and rounds and stores its sums while the first stages of tile `nt` are copied.
 // (One body for every NP, with the rows behind conditions, made the compiler move the sums
 // between register files.)
-template <bool SWIGLU, int NP>
-__device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies &c,
+template <typename G, int NP>
+__device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies<G> &c,
                                         bool more, const MxTile &nt, const MxLds &l) {
+    constexpr bool SWIGLU = G::SWIGLU;
     constexpr int F = SWIGLU ? 2 : 1;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -376,34 +292,19 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     const bool half = p.Kred % 256 != 0;  // of the last stage's row pieces the second halves alone
 
     const int r = lane & 31, g = lane >> 5;
-    int frag_off[4];  // lane's place in 32 rows of a stage, 64 of the reduction each
+    int place[4];  // of the lane in a row of a stage, 64 of the reduction each
 #pragma unroll
-    for (int h = 0; h < 4; ++h) frag_off[h] = r * 128 + mx_swz(r, 2 * h + g) * 16;
-    // LDS addresses of stage s, tile row 0
-    auto codes = [&](int s) { return l.data + (s & 1) * kMxStageBytes; };
-    auto scales = [&](int s) {
-        return l.scale + ((s >> 1) & 1) * kMxScaleBytes + r * 16 + mx_start(s, 8, p.Kred / 32) -
-               mx_start(s >> 1, 16, p.Kred / 32);
-    };
-    // 32 rows of a stage: four fragments, and the rows' eight scale bytes
-    auto read = [&](const uint8_t *q, const uint8_t *x, int row, v4i (&f)[4], int (&sc)[2]) {
+    for (int h = 0; h < 4; ++h) place[h] = mx_swz(r, 2 * h + g) * 16;
+    auto read_w = [&](const MxStage<G> &st, v4i (&f)[2][4], int (&sc)[2][2]) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-            f[h] = *reinterpret_cast<const v4i *>(q + row * 128 + frag_off[h]);
-        sc[0] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
-        sc[1] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16 + 4);
-    };
-    auto read_w = [&](int s, v4i (&f)[2][4], int (&sc)[2][2]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            read(codes(s), scales(s), kMxTile + wave * 64 + 32 * j, f[j], sc[j]);
+        for (int j = 0; j < 2; ++j) st.read(G::AR + wave * 64 + 32 * j, place, f[j], sc[j]);
     };
     v16f acc[NP][2] = {};
     v4i w[2][4], a[2][4];  // weights of the stage, rows of the two fragments that are multiplied
     int wsc[2][2], asc[2][2];
-    auto read_a = [&](const uint8_t *q, const uint8_t *x, int pair, v4i (&f)[2][4], int (&sc)[2][2]) {
+    auto read_a = [&](const MxStage<G> &st, int pair, v4i (&f)[2][4], int (&sc)[2][2]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) read(q, x, 64 * pair + 32 * i, f[i], sc[i]);
+        for (int i = 0; i < 2; ++i) st.read(64 * pair + 32 * i, place, f[i], sc[i]);
     };
     // Two row fragments by two weight fragments: four sums that take turns, so that no product
     // waits for the one before it.  (With two, the loop ran at half the rate.)
@@ -412,10 +313,10 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         for (int i = 0; i < 2; ++i) {
             asc[i][0] >>= 8 * g;  // the lane's blocks are g and 2 + g of each half
             asc[i][1] >>= 8 * g;
-            // Codes of 0 where the first half has been multiplied before.  (A NaN scale makes a
-            // NaN of them, but where it did so before.)
+            // codes of 0, and no NaN for a scale, where the first half is not to be multiplied
             a[i][0] &= first_half;
             a[i][1] &= first_half;
+            asc[i][0] &= first_half;
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h)
@@ -437,15 +338,18 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
 
     // Each pair of fragments is read while the one before is multiplied; a stage's first pair and
     // weights while the stage before multiplies its last.
-    read_w(0, w, wsc);
-    read_a(codes(0), scales(0), 0, a, asc);
+    {
+        const MxStage<G> st(p, l, 0, 0);
+        read_w(st, w, wsc);
+        read_a(st, 0, a, asc);
+    }
 #pragma unroll 1
     for (int s = 0; s < ns; ++s) {
-        const uint8_t *q = codes(s), *x = scales(s);
+        const MxStage<G> st(p, l, s, s & 1);
         const int first_half = half && s + 1 == ns ? 0 : -1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            wsc[j][0] >>= 8 * g;
+            wsc[j][0] = wsc[j][0] >> (8 * g) & first_half;
             wsc[j][1] >>= 8 * g;
         }
         v4i na[2][4];
@@ -461,7 +365,7 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         };
 #pragma unroll
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
-            read_a(q, x, pair + 1, na, nasc);
+            read_a(st, pair + 1, na, nasc);
             __builtin_amdgcn_sched_barrier(0);
             multiply(pair, first_half);
             __builtin_amdgcn_sched_barrier(0);
@@ -472,9 +376,10 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         if (s + 1 < ns) {
             wait_vmcnt<0>();  // stage s + 1
             __syncthreads();
-            if (s + 2 < ns) mx_issue<NP>(p, c, l, s + 2);
-            read_w(s + 1, nw, nwsc);
-            read_a(codes(s + 1), scales(s + 1), 0, na, nasc);
+            if (s + 2 < ns) mx_issue<G, NP>(p, c, l, s + 2, s & 1);
+            const MxStage<G> next(p, l, s + 1, (s + 1) & 1);
+            read_w(next, nw, nwsc);
+            read_a(next, 0, na, nasc);
         }
         __builtin_amdgcn_sched_barrier(0);
         multiply(NP / 2 - 1, first_half);
@@ -491,9 +396,10 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
 
     if (more) {
         __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
-        c = mx_copies<SWIGLU>(p, nt, l);
-        mx_issue<0>(p, c, l, 0);
-        mx_issue<0>(p, c, l, 1);
+        c = mx_copies<G>(p, nt, l, 2);
+        mx_short_scales<G>(p, nt, c, l);
+        mx_issue<G, 0>(p, c, l, 0, 0);
+        if (ns > 1) mx_issue<G, 0>(p, c, l, 1, 1);
     }
     // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
     // that each holds eight columns in a row and stores 16 bytes.
@@ -522,7 +428,7 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             }
     }
     __builtin_amdgcn_sched_barrier(0);
-    const int n0 = t.nblk * (kMxTile / F) + wave * (64 / F);
+    const int n0 = t.nblk * G::COLS + wave * (64 / F);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int row = 32 * i + r;
@@ -542,24 +448,25 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         // The first stage's copies are older than the second's, 10 at least, and than the stores:
         // all but the last two fragments have whole rows, so at least that many were issued,
         // unless columns past N were left out.
-        if (n0 + 64 / F <= p.N) wait_vmcnt<10 + (NP - 2) * J * 2>();
+        if (ns == 1) wait_vmcnt<0>();
+        else if (n0 + 64 / F <= p.N) wait_vmcnt<10 + (NP - 2) * J * 2>();
         else wait_vmcnt<10>();
         __syncthreads();
     }
 }
 
 template <bool SWIGLU>
-__global__ __launch_bounds__(kMxTileThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+__global__ __launch_bounds__(kMxThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void
 mxfp4_gmm_tile_kernel(MxGmmParams p) {
-    constexpr int COLS = kMxTile / (SWIGLU ? 2 : 1);  // output columns of a tile
+    typedef MxGeom<SWIGLU, 256, 256> G;
     __shared__ int s_w[4];
     __shared__ MxSchedule s_s;
     __shared__ MxTile s_t[kMxList];
-    __shared__ int32_t s_route[kMxTile];
-    __shared__ __align__(16) uint8_t s_data[2 * kMxStageBytes];
-    __shared__ __align__(16) uint8_t s_scale[2 * kMxScaleBytes];
+    __shared__ int32_t s_route[G::AR];
+    __shared__ __align__(16) uint8_t s_data[2 * G::STAGE];
+    __shared__ __align__(16) uint8_t s_scale[16 + 2 * G::SCALE];  // a short row's word may start 4 bytes early
 
-    mx_schedule(p, (p.N + COLS - 1) / COLS, s_w, s_s);
+    mx_schedule<G>(p, s_w, s_s);
     const int total = __builtin_amdgcn_readfirstlane(s_s.total);
     // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share
     // weight and row blocks in its L2
@@ -569,9 +476,8 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     const int n = t0 < t1 ? (t1 - t0 + step - 1) / step : 0;  // tiles of this workgroup
     if (n == 0) return;
 
-    const MxLds l{s_data, s_scale, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
-                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale)),
-                  s_route};
+    const MxLds l{s_data, s_scale + 16, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route};
     const int tid = threadIdx.x;
     const uint32_t route_at =
         __builtin_amdgcn_readfirstlane(lds_addr(s_route) + (tid >> 6) * (kWave * 4));
@@ -580,55 +486,179 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     };
     // its tiles are looked up kMxList at a time, a lane each
     auto look_up = [&](int k) {
-        if (tid < kMxList && k + tid < n) s_t[tid] = mx_find_tile(s_s, t0 + (k + tid) * step);
+        if (tid < kMxList && k + tid < n) s_t[tid] = mx_find_tile<G>(s_s, t0 + (k + tid) * step);
         __syncthreads();
     };
-    auto tile = [&](int k) {
-        const MxTile &x = s_t[k % kMxList];
-        return MxTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.row0),
-                      __builtin_amdgcn_readfirstlane(x.rows), __builtin_amdgcn_readfirstlane(x.nblk)};
-    };
     look_up(0);
-    MxTile cur = tile(0);
+    MxTile cur = mx_uniform(s_t[0]);
     fetch_routes(cur);
     wait_vmcnt<0>();
     __syncthreads();
-    MxCopies c = mx_copies<SWIGLU>(p, cur, l);
-    mx_issue<0>(p, c, l, 0);
-    mx_issue<0>(p, c, l, 1);  // at least 2 stages
-    wait_vmcnt<10>();
+    MxCopies<G> c = mx_copies<G>(p, cur, l, 2);
+    mx_short_scales<G>(p, cur, c, l);
+    mx_issue<G, 0>(p, c, l, 0, 0);
+    if (p.Kred > 256) {
+        mx_issue<G, 0>(p, c, l, 1, 1);
+        wait_vmcnt<10>();
+    } else {
+        wait_vmcnt<0>();
+    }
     __syncthreads();
     for (int k = 1;; ++k) {
         const bool more = k < n;
         if (more && k % kMxList == 0) look_up(k);  // the last tiles of the list have been read
-        const MxTile next = more ? tile(k) : cur;
+        const MxTile next = more ? mx_uniform(s_t[k % kMxList]) : cur;
         if (more) fetch_routes(next);
-        if (cur.rows > 192) mx_tile<SWIGLU, 8>(p, cur, c, more, next, l);
-        else if (cur.rows > 128) mx_tile<SWIGLU, 6>(p, cur, c, more, next, l);
-        else if (cur.rows > 64) mx_tile<SWIGLU, 4>(p, cur, c, more, next, l);
-        else mx_tile<SWIGLU, 2>(p, cur, c, more, next, l);
+        if (cur.rows > 192) mx_tile<G, 8>(p, cur, c, more, next, l);
+        else if (cur.rows > 128) mx_tile<G, 6>(p, cur, c, more, next, l);
+        else if (cur.rows > 64) mx_tile<G, 4>(p, cur, c, more, next, l);
+        else mx_tile<G, 2>(p, cur, c, more, next, l);
         if (!more) return;
         cur = next;
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows per expert: the product streams weights.  Tiles of at most 64 rows by 128
+// weight rows; two workgroups fit a CU, so that one copies while the other looks up its tile,
+// waits for its first stage or stores.  Three slots: two stages are under way while one is
+// multiplied.
+template <typename G, int NP>
+__device__ __forceinline__ void mx_narrow(const MxGmmParams &p, const MxTile &t, const MxCopies<G> &c,
+                                          const MxLds &l) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ns = (p.Kred + 255) / 256;
+    const int r = lane & 31, g = lane >> 5;
+    int place[4];  // of the lane in a row of a stage, 64 of the reduction each
+#pragma unroll
+    for (int h = 0; h < 4; ++h) place[h] = mx_swz(r, 2 * h + g) * 16;
+
+    v16f acc[NP] = {};
+    int slot = 0;
+#pragma unroll 1
+    for (int s = 0; s < ns; ++s) {
+        if (s + 1 < ns) wait_vmcnt<G::WC + NP>();  // all but the last copies of stage s + 1
+        else wait_vmcnt<0>();
+        __syncthreads();  // and every wave has read stage s - 1, whose slot is the next
+        const int free = slot == 0 ? 2 : slot - 1;
+        if (s + 2 < ns) mx_issue<G, NP>(p, c, l, s + 2, free);
+        const MxStage<G> st(p, l, s, slot);
+        v4i w[4], a[NP][4];
+        int wsc[2], asc[NP][2];
+        st.read(G::AR + wave * 32, place, w, wsc);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) st.read(32 * i, place, a[i], asc[i]);
+        // of the last stage, where the reduction ends in it, the second halves of the pieces alone
+        const int first_half = s + 1 == ns && p.Kred % 256 != 0 ? 0 : -1;
+        // the lane's blocks are g and 2 + g of each half
+        wsc[0] = wsc[0] >> (8 * g) & first_half;
+        wsc[1] >>= 8 * g;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            a[i][0] &= first_half;
+            a[i][1] &= first_half;
+            asc[i][0] = asc[i][0] >> (8 * g) & first_half;
+            asc[i][1] >>= 8 * g;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+                acc[i] = h & 1 ? mx_mfma32<1>(w[h], wsc[h >> 1], a[i][h], asc[i][h >> 1], acc[i])
+                               : mx_mfma32<0>(w[h], wsc[h >> 1], a[i][h], asc[i][h >> 1], acc[i]);
+        slot = slot == 2 ? 0 : slot + 1;
+    }
+
+    // four columns a lane, rounded; lanes l and l + 32 exchange halves as above
+    constexpr int GR = G::SWIGLU ? 2 : 4;
+    const int n0 = t.nblk * G::COLS + wave * (G::COLS / 4);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        uint2 out[GR];
+#pragma unroll
+        for (int k = 0; k < GR; ++k) {
+            float y[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                y[v] = G::SWIGLU ? mx_silu_times(acc[i][4 * k + v], acc[i][8 + 4 * (k & 1) + v])
+                                 : acc[i][4 * k + v];
+            out[k] = G::SWIGLU ? make_uint2(f2bf_pk(y[0], y[1]), f2bf_pk(y[2], y[3]))
+                               : make_uint2(f2h(y[0]) | (uint32_t)f2h(y[1]) << 16,
+                                            f2h(y[2]) | (uint32_t)f2h(y[3]) << 16);
+        }
+        const int row = 32 * i + r;
+        uint16_t *crow = p.c + (size_t)(t.row0 + row) * p.N;
+#pragma unroll
+        for (int k = 0; k < GR; k += 2) {
+            const auto x = __builtin_amdgcn_permlane32_swap(out[k].x, out[k + 1].x, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(out[k].y, out[k + 1].y, false, false);
+            const int col = n0 + 8 * (k + g);
+            if (row < t.rows && col < p.N)
+                *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+        }
+    }
+}
+
 template <bool SWIGLU>
-static void launch_tile(const MxGmmParams &p, int cu_count, hipStream_t stream) {
-    const int cols = kMxTile / (SWIGLU ? 2 : 1);
-    // at most this many tiles; one workgroup fits a CU
-    const long long most =
-        ((long long)p.R / kMxTile + (p.E < p.R ? p.E : p.R)) * ((p.N + cols - 1) / cols);
-    const long long g = most < cu_count ? most : cu_count;
-    hipLaunchKernelGGL(mxfp4_gmm_tile_kernel<SWIGLU>, dim3((unsigned)((g + 7) / 8 * 8)),
-                       dim3(kMxTileThreads), 0, stream, p);
+__global__ __launch_bounds__(kMxThreads) __attribute__((amdgpu_waves_per_eu(2))) void
+mxfp4_gmm_narrow_kernel(MxGmmParams p) {
+    typedef MxGeom<SWIGLU, 64, 128> G;
+    __shared__ int s_w[4];
+    __shared__ MxTile s_t;
+    __shared__ int32_t s_route[G::AR];
+    __shared__ __align__(16) uint8_t s_data[3 * G::STAGE];
+    __shared__ __align__(16) uint8_t s_scale[16 + 2 * G::SCALE];  // a short row's word may start 4 bytes early
+
+    // the schedule is only looked at here, before the first copies: it lies where they go
+    MxSchedule &s_s = *reinterpret_cast<MxSchedule *>(s_data);
+    mx_schedule<G>(p, s_w, s_s);
+    // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles
+    const int total = __builtin_amdgcn_readfirstlane(s_s.total), per = (total + 7) / 8;
+    const int t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || t >= total) return;
+    const int tid = threadIdx.x;
+    if (tid == 0) s_t = mx_find_tile<G>(s_s, t);
+    __syncthreads();
+    const MxTile tile = mx_uniform(s_t);
+    const MxLds l{s_data, s_scale + 16, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route};
+    if (p.a_route && tid < G::AR) s_route[tid] = p.a_route[tile.row0 + min(tid, tile.rows - 1)];
+    __syncthreads();
+    const MxCopies<G> c = mx_copies<G>(p, tile, l, 1);
+    mx_short_scales<G>(p, tile, c, l);
+    mx_issue<G, 0>(p, c, l, 0, 0);
+    if (p.Kred > 256) mx_issue<G, 0>(p, c, l, 1, 1);
+    if (tile.rows > 32) mx_narrow<G, 2>(p, tile, c, l);
+    else mx_narrow<G, 1>(p, tile, c, l);
+}
+
+// the tiles of a geometry, at most
+template <typename G>
+static long long mx_most_tiles(const MxGmmParams &p) {
+    return ((long long)p.R / G::AR + (p.E < p.R ? p.E : p.R)) * ((p.N + G::COLS - 1) / G::COLS);
+}
+
+template <bool SWIGLU>
+static void launch_variant(const MxGmmParams &p, bool narrow, int cu_count, hipStream_t stream) {
+    if (narrow) {
+        const long long n = (mx_most_tiles<MxGeom<SWIGLU, 64, 128>>(p) + 7) / 8 * 8;
+        hipLaunchKernelGGL(mxfp4_gmm_narrow_kernel<SWIGLU>, dim3((unsigned)n), dim3(kMxThreads), 0, stream, p);
+    } else {
+        const long long n = mx_most_tiles<MxGeom<SWIGLU, 256, 256>>(p);  // one workgroup fits a CU
+        hipLaunchKernelGGL(mxfp4_gmm_tile_kernel<SWIGLU>, dim3((unsigned)((n < cu_count ? n : cu_count) + 7) / 8 * 8),
+                           dim3(kMxThreads), 0, stream, p);
+    }
 }
 
 hipError_t launch_mxfp4_gmm(const MxGmmParams &p, bool swiglu, int cu_count, hipStream_t stream) {
     const int mean = (p.R + p.E - 1) / p.E;
-    // the tiles' scale copies take 16 bytes of a row
-    const bool tiles = mean > 32 && p.Kred >= 512;
-    if (swiglu) tiles ? launch_tile<true>(p, cu_count, stream) : launch_stream<true>(p, stream);
-    else tiles ? launch_tile<false>(p, cu_count, stream) : launch_stream<false>(p, stream);
+    // Measured on both sides, gmm1 / gmm2 at K = 7168, I = 2048, E = 32, top_k = 8, in us: 1 token
+    // narrow 24 / 12, wide 44 / 16; 32 mean rows 96 / 56 and 103 / 60; 50 rows 110 / 60 and 108 / 64;
+    // 64 rows 130 / 70 and 114 / 70.  At K = 4096, I = 1408, E = 64, 48 mean rows: 83 / 53 and 85 / 56.
+    const bool narrow = mean <= 48;
+    if (swiglu) launch_variant<true>(p, narrow, cu_count, stream);
+    else launch_variant<false>(p, narrow, cu_count, stream);
     return hipGetLastError();
 }
 
