@@ -327,6 +327,29 @@ def _type(t: torch.Tensor) -> int:
     return _TYPES[t.dtype]
 
 
+def _launch(name: str, tensors, args, stream) -> None:
+    """Calls the entry point `name` with args and the stream, on the device of the tensors: all
+    have to lie there, whichever device is current.  Without a stream, that device's current one."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors must be on one device")
+    if stream is None:  # the same handle as torch.cuda.current_stream(dev).cuda_stream, sooner
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError("the stream must be on the tensors' device")
+    else:
+        handle = stream.cuda_stream
+    fn = getattr(_lib or load(), name)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != MEGAMOE_OK:
+        raise MegaMoEError(name, rc)
+
+
 def _shape(name: str, t: torch.Tensor, *shape: int) -> None:
     if tuple(t.shape) != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
@@ -338,10 +361,9 @@ def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, str
     _shape("probs", probs, d.M, d.top_k)
     if bias is not None:
         _shape("bias", bias, d.E)
-    _check("megamoe_route", load().megamoe_route(
-        ctypes.byref(d), _ptr(logits), _type(logits), _ptr(bias, torch.float32),
-        int(bool(renormalize)), _ptr(expert_idx, torch.int32), _ptr(probs, torch.float32),
-        _stream(stream)))
+    args = (ctypes.byref(d), _ptr(logits), _type(logits), _ptr(bias, torch.float32),
+            int(bool(renormalize)), _ptr(expert_idx, torch.int32), _ptr(probs, torch.float32))
+    _launch("megamoe_route", (logits, bias, expert_idx, probs), args, stream)
 
 
 def megamoe_few_workspace_bytes(d: megamoe_dims) -> int:
@@ -357,11 +379,12 @@ def megamoe_forward_few(d, x, expert_idx, probs, w1p, scale1, w2p, scale2, out, 
     _shape("expert_idx", expert_idx, d.M, d.top_k)
     _shape("probs", probs, d.M, d.top_k)
     _shape("out", out, d.M, d.K)
-    _check("megamoe_forward_few", load().megamoe_forward_few(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
-        _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(out, torch.bfloat16),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    args = (ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
+            _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
+            _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(out, torch.bfloat16),
+            _ptr(workspace), workspace.numel() * workspace.element_size())
+    _launch("megamoe_forward_few", (x, expert_idx, probs, w1p, scale1, w2p, scale2, out, workspace),
+            args, stream)
 
 
 def _rows_cols(x: torch.Tensor) -> tuple[int, int]:
@@ -382,17 +405,17 @@ def megamoe_mxfp4_quant(x, q, scale, valid_rows=None, stream=None):
     [rows, cols / 32].  valid_rows: int32 device tensor of one element."""
     rows, cols = _rows_cols(x)
     _mx_rows(q, scale, rows, cols, valid_rows)
-    _check("megamoe_mxfp4_quant", load().megamoe_mxfp4_quant(
-        _ptr(x), _type(x), rows, cols, _ptr(valid_rows, torch.int32), _ptr(q, torch.uint8),
-        _ptr(scale, torch.uint8), _stream(stream)))
+    args = (_ptr(x), _type(x), rows, cols, _ptr(valid_rows, torch.int32), _ptr(q, torch.uint8),
+            _ptr(scale, torch.uint8))
+    _launch("megamoe_mxfp4_quant", (x, q, scale, valid_rows), args, stream)
 
 
 def megamoe_mxfp4_dequant(q, scale, x, valid_rows=None, stream=None):
     rows, cols = _rows_cols(x)
     _mx_rows(q, scale, rows, cols, valid_rows)
-    _check("megamoe_mxfp4_dequant", load().megamoe_mxfp4_dequant(
-        _ptr(q, torch.uint8), _ptr(scale, torch.uint8), rows, cols,
-        _ptr(valid_rows, torch.int32), _ptr(x), _type(x), _stream(stream)))
+    args = (_ptr(q, torch.uint8), _ptr(scale, torch.uint8), rows, cols,
+            _ptr(valid_rows, torch.int32), _ptr(x), _type(x))
+    _launch("megamoe_mxfp4_dequant", (q, scale, x, valid_rows), args, stream)
 
 
 def _mx_weights(name: str, d, q: torch.Tensor, s: torch.Tensor, rows: int, cols: int) -> None:
@@ -407,11 +430,10 @@ def megamoe_mxfp4_gmm1(d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, stre
     _shape("expert_cumsum", expert_cumsum, d.E)
     _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
     _shape("y", y, R, d.I)
-    _check("megamoe_mxfp4_gmm1", load().megamoe_mxfp4_gmm1(
-        ctypes.byref(d), _ptr(xq, torch.uint8), _ptr(xs, torch.uint8),
-        _ptr(sorted_route, torch.int32), _ptr(expert_cumsum, torch.int32),
-        _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8), _ptr(y, torch.bfloat16),
-        _stream(stream)))
+    args = (ctypes.byref(d), _ptr(xq, torch.uint8), _ptr(xs, torch.uint8),
+            _ptr(sorted_route, torch.int32), _ptr(expert_cumsum, torch.int32),
+            _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8), _ptr(y, torch.bfloat16))
+    _launch("megamoe_mxfp4_gmm1", (xq, xs, sorted_route, expert_cumsum, w1q, w1s, y), args, stream)
 
 
 def megamoe_mxfp4_gmm2(d, yq, ys, expert_cumsum, w2q, w2s, gmm2_out, stream=None):
@@ -420,10 +442,10 @@ def megamoe_mxfp4_gmm2(d, yq, ys, expert_cumsum, w2q, w2s, gmm2_out, stream=None
     _shape("expert_cumsum", expert_cumsum, d.E)
     _mx_weights("w2", d, w2q, w2s, d.K, d.I)
     _shape("gmm2_out", gmm2_out, R, d.K)
-    _check("megamoe_mxfp4_gmm2", load().megamoe_mxfp4_gmm2(
-        ctypes.byref(d), _ptr(yq, torch.uint8), _ptr(ys, torch.uint8),
-        _ptr(expert_cumsum, torch.int32), _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8),
-        _ptr(gmm2_out, torch.float16), _stream(stream)))
+    args = (ctypes.byref(d), _ptr(yq, torch.uint8), _ptr(ys, torch.uint8),
+            _ptr(expert_cumsum, torch.int32), _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8),
+            _ptr(gmm2_out, torch.float16))
+    _launch("megamoe_mxfp4_gmm2", (yq, ys, expert_cumsum, w2q, w2s, gmm2_out), args, stream)
 
 
 def megamoe_mxfp4_workspace_bytes(d: megamoe_dims) -> int:
@@ -441,11 +463,12 @@ def megamoe_forward_mxfp4(d, x, expert_idx, probs, w1q, w1s, w2q, w2s, out, work
     _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
     _mx_weights("w2", d, w2q, w2s, d.K, d.I)
     _shape("out", out, d.M, d.K)
-    _check("megamoe_forward_mxfp4", load().megamoe_forward_mxfp4(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(probs, torch.float32), _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8),
-        _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8), _ptr(out, torch.bfloat16),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    args = (ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
+            _ptr(probs, torch.float32), _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8),
+            _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8), _ptr(out, torch.bfloat16),
+            _ptr(workspace), workspace.numel() * workspace.element_size())
+    _launch("megamoe_forward_mxfp4", (x, expert_idx, probs, w1q, w1s, w2q, w2s, out, workspace),
+            args, stream)
 
 
 def megamoe_set_overlap(mode: int) -> None:
