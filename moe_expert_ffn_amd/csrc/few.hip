@@ -124,9 +124,10 @@ __device__ __forceinline__ v4i few_mfma(v4i w, v4i a, v4i acc) {
 // ---------------------------------------------------------------------------
 constexpr int kFew1Groups = 2;  // groups of 16 columns that share the quantised rows
 
+template <int U>  // K slices a wave has in flight
 __global__ __launch_bounds__(kFewThreads) __attribute__((amdgpu_waves_per_eu(4))) void
 few_gmm1_kernel(FewParams p, int row_cap) {
-    constexpr int NG = kFew1Groups, U = 7;  // U: K slices a wave has in flight
+    constexpr int NG = kFew1Groups;
     __shared__ FewPairs s_p;
     __shared__ int s_tok[16];
     __shared__ uint32_t s_red[16][kFewWaves];
@@ -277,14 +278,15 @@ few_gmm1_kernel(FewParams p, int row_cap) {
 
 // ---------------------------------------------------------------------------
 // The second product.  A workgroup works through steps, each a run of experts
-// whose rows fit an LDS buffer (and a chunk of I where I is long).  Half of its
-// waves quantise the rows of the next step while the other half multiplies the
-// current one, so weights keep coming while y is read and rounded; with all
-// waves doing both in turn the kernel took 125 us at 16 tokens (K = 7168, I = 2048,
-// E = 32, top_k = 8) and 26.6 at one.
+// whose rows fit an LDS buffer (and a chunk of I where I is long).  Twelve of its
+// waves quantise the rows of the next step while four multiply the current one,
+// so weights keep coming while y is read and rounded.  (K = 7168, I = 2048, E = 32,
+// top_k = 8: 92 us at 16 tokens and 23.5 at one, of 71 and 18 for the weights
+// alone; eight and eight waves took 100 and 23.4, all waves doing both in turn
+// 125 and 26.6.)
 constexpr int kFew2Threads = 1024;
-constexpr int kFew2Waves = kFew2Threads / kWave / 2;  // of either kind
-constexpr int kFew2Cols = 32;
+constexpr int kFew2Mul = 4;                                 // waves that multiply
+constexpr int kFew2Quant = kFew2Threads / kWave - kFew2Mul;  // and that quantise
 
 // A barrier of all waves that each kind reaches at a place of its own.
 __device__ __forceinline__ void few_barrier() {
@@ -311,10 +313,12 @@ __device__ __forceinline__ FewStep few_step(const FewPairs &s, int n_act, int a0
     return t;
 }
 
+template <int COLS>  // output columns of a workgroup, 16 or 32
 __global__ __launch_bounds__(kFew2Threads) __attribute__((amdgpu_waves_per_eu(4))) void
 few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
-    constexpr int U = 8;        // K slices a wave has in flight
-    constexpr int NS = 8;       // channel scales a quantising thread fetches early
+    constexpr int H = COLS / 16;  // weight fragments of a K slice
+    constexpr int U = 16 / H;     // K slices a wave has in flight
+    constexpr int NS = 8;         // channel scales a quantising thread fetches early
     __shared__ FewPairs s_p;
     __shared__ int s_id[kFewThreads];
     __shared__ v4i s_zero[4];
@@ -323,17 +327,17 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool multiplies = wave < kFew2Waves;
-    const int hw = multiplies ? wave : wave - kFew2Waves;
+    const bool multiplies = wave < kFew2Mul;
+    const int hw = multiplies ? wave : wave - kFew2Mul;
     const int K = p.K, I = p.I, R = p.M * p.top_k, stride = i_cap + 16;
-    int *s_acc = reinterpret_cast<int *>(s_dyn);               // [R][32], int32 then fp32
-    int8_t *s_a = s_dyn + (size_t)R * kFew2Cols * 4;           // 2 x [row_cap][i_cap + 16]
+    int *s_acc = reinterpret_cast<int *>(s_dyn);               // [R][COLS], int32 then fp32
+    int8_t *s_a = s_dyn + (size_t)R * COLS * 4;           // 2 x [row_cap][i_cap + 16]
     few_find_pairs<kFew2Threads>(p.expert_idx, R, p.E, p.top_k, s_p);
     const int n_act = __builtin_amdgcn_readfirstlane(s_p.n_act), n_pair = s_p.n_pair;
 
     const int NB = (K + kPackRowsF - 1) / kPackRowsF;
     const size_t block = (size_t)NB * kPackBlockF, slice = (size_t)p.E * block;
-    const int n0 = few_group(blockIdx.x, gridDim.x) * kFew2Cols;
+    const int n0 = few_group(blockIdx.x, gridDim.x) * COLS;
     const int8_t *w0 = p.w2p + (size_t)(n0 / kPackRowsF) * kPackBlockF + (n0 % kPackRowsF) * 64;
     const uint32_t woff = (lane & 15) * 64 + (lane >> 4) * 16;
     const v4i zero = {0, 0, 0, 0};
@@ -341,15 +345,15 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
     FewStep cur = few_step(s_p, n_act, 0, 0, 0, I, row_cap, i_cap);
     // multiplying waves: a ring of U K slices in registers, as above, of the wave's shares of the
     // steps' (expert, K slice) lists
-    v4i f[U][2];
+    v4i f[U][H];
     FewStep to = cur;        // the step whose slices are loaded now
     int ti = 0, te = 0;      // the next of the wave's share of it, and the share's end
     int la = 0, ls = 0;      // the same as expert and slice
     const int8_t *lq = w0;   // and its address
     auto share = [&](const FewStep &t, int &t0, int &t1) {
         const int T = (t.a1 - t.a0) * (t.ic / 64);
-        t0 = hw * T / kFew2Waves;
-        t1 = (hw + 1) * T / kFew2Waves;
+        t0 = hw * T / kFew2Mul;
+        t1 = (hw + 1) * T / kFew2Mul;
     };
     auto expert = [&]() {
         lq = uniform_ptr(w0 + (size_t)(to.i0 / 64 + ls) * slice + s_p.act[la] * block);
@@ -363,8 +367,8 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
         expert();
     };
     auto load = [&](int u) {
-        f[u][0] = few_load(lq, woff);
-        f[u][1] = few_load(lq + 1024, woff);
+#pragma unroll
+        for (int h = 0; h < H; ++h) f[u][h] = few_load(lq + 1024 * h, woff);
         if (ti + 1 < te) {
             ++ti;
             if (++ls == to.ic / 64) {
@@ -378,16 +382,16 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
     };
     // the channel scale of element i of the accumulators (pair i / 32, column i % 32)
     auto channel_scale = [&](int i) {
-        const int pr = i / kFew2Cols;
+        const int pr = i / COLS;
         int lo = 0, hi = n_act - 1;  // the pair's expert: the first one that ends after it
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s_p.end[mid] > pr) hi = mid;
             else lo = mid + 1;
         }
-        return p.scale2[(size_t)s_p.act[lo] * K + n0 + i % kFew2Cols];
+        return p.scale2[(size_t)s_p.act[lo] * K + n0 + i % COLS];
     };
-    const int htid = tid & (kFew2Threads / 2 - 1), n_out = n_pair * kFew2Cols;
+    const int htid = hw * kWave + lane, n_out = n_pair * COLS;
     int8_t *buf = s_a, *other = s_a + (size_t)row_cap * stride;
     auto after = [&](const FewStep &t) {  // the same experts' next chunk, or the next experts
         const bool more = t.i0 + t.ic < I;
@@ -407,7 +411,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             for (int u = 0; u < U; ++u) load(u);
         }
         if (tid < 4) s_zero[tid] = zero;
-        for (int i = htid; i < n_out; i += kFew2Threads / 2) s_acc[i] = 0;
+        for (int i = htid; i < n_out; i += kFew2Mul * kWave) s_acc[i] = 0;
         few_barrier();
         while (cur.a0 < n_act) {
             const FewStep nxt = after(cur);
@@ -416,7 +420,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             share(cur, t0, t1);
             int ca = __builtin_amdgcn_readfirstlane(cur.a0 + t0 / nsl);
             int cs = __builtin_amdgcn_readfirstlane(t0 % nsl);
-            v4i acc[2] = {zero, zero};
+            v4i acc[H] = {};
             int rows = 0, prow = 0;
             const int8_t *arow = buf, *zrow = reinterpret_cast<const int8_t *>(&s_zero[lane >> 4]);
             auto open = [&]() {
@@ -428,21 +432,22 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             };
             auto flush = [&]() {  // integer sums: the order of the waves does not matter
                 if ((lane & 15) < rows) {
-                    int *d = s_acc + (prow + (lane & 15)) * kFew2Cols + 4 * (lane >> 4);
+                    int *d = s_acc + (prow + (lane & 15)) * COLS + 4 * (lane >> 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < H; ++h)
 #pragma unroll
                         for (int v = 0; v < 4; ++v) atomicAdd(d + 16 * h + v, acc[h][v]);
                 }
-                acc[0] = acc[1] = zero;
+#pragma unroll
+                for (int h = 0; h < H; ++h) acc[h] = zero;
             };
             auto batch = [&](auto refill, int t) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const v4i a =
                         *reinterpret_cast<const v4i *>(t + u < t1 ? arow + cs * 64 : zrow);
-                    acc[0] = few_mfma(f[u][0], a, acc[0]);
-                    acc[1] = few_mfma(f[u][1], a, acc[1]);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) acc[h] = few_mfma(f[u][h], a, acc[h]);
                     if constexpr (refill.value) load(u);
                     if (t + u < t1 && ++cs == nsl) {
                         flush();
@@ -482,7 +487,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             const size_t pr = fs.p0 + fr;
             const float4 *y = reinterpret_cast<const float4 *>(p.y + pr * I + fs.i0);
             const float *ym = p.ymax + pr * (I / 16);
-            fr += kFew2Waves;
+            fr += kFew2Quant;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 if (c * kWave + lane < fs.ic / 4) next[c] = y[c * kWave + lane];
@@ -490,7 +495,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             for (int c = lane + kWave; c < I / 16; c += kWave) next_big = fmaxf(next_big, ym[c]);
         };
         auto quantise = [&](const FewStep &t, int8_t *dst_rows) {
-            for (int row = hw; row < t.p1 - t.p0; row += kFew2Waves) {
+            for (int row = hw; row < t.p1 - t.p0; row += kFew2Quant) {
                 float4 v[8];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] = next[c];
@@ -514,7 +519,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             }
         };
         fetch();
-        for (int i = htid; i < R; i += kFew2Threads / 2) {
+        for (int i = htid; i < R; i += kFew2Quant * kWave) {
             s_id[i] = p.expert_idx[i];
             s_prob[i] = p.probs[i];
         }
@@ -528,7 +533,7 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
             } else {  // the channel scales, while the last step is multiplied
 #pragma unroll
                 for (int k = 0; k < NS; ++k) {
-                    const int i = htid + k * (kFew2Threads / 2);
+                    const int i = htid + k * (kFew2Quant * kWave);
                     sc[k] = i < n_out ? channel_scale(i) : 0.0f;
                 }
             }
@@ -539,26 +544,26 @@ few_gmm2_kernel(FewParams p, int row_cap, int i_cap) {
         // dequantise every pair's columns in place
         auto dequant = [&](int i, float scale) {
             const uint16_t h = f2h(keep_f32((float)s_acc[i] * scale));
-            const float g = __builtin_fmaf(h2f(h), s_pts2[i / kFew2Cols], 0.0f);
+            const float g = __builtin_fmaf(h2f(h), s_pts2[i / COLS], 0.0f);
             s_acc[i] = (int)__float_as_uint(bf2f_lo(f2bf_pk(g, 0.0f)));
         };
 #pragma unroll
         for (int k = 0; k < NS; ++k) {
-            const int i = htid + k * (kFew2Threads / 2);
+            const int i = htid + k * (kFew2Quant * kWave);
             if (i < n_out) dequant(i, sc[k]);
         }
-        for (int i = htid + NS * (kFew2Threads / 2); i < n_out; i += kFew2Threads / 2)
+        for (int i = htid + NS * (kFew2Quant * kWave); i < n_out; i += kFew2Quant * kWave)
             dequant(i, channel_scale(i));
     }
     __syncthreads();
-    if (tid < p.M * kFew2Cols) {  // slots in order, multiply then add
-        const int t = tid / kFew2Cols, col = tid % kFew2Cols;
+    if (tid < p.M * COLS) {  // slots in order, multiply then add
+        const int t = tid / COLS, col = tid % COLS;
         float acc = 0.0f;
         for (int s = 0; s < p.top_k; ++s) {
             const int e = s_id[t * p.top_k + s];
             if (e < 0 || e >= p.E) continue;
             const int pr = s_p.base[e] + __popc(s_p.mask[e] & ((1u << t) - 1));
-            acc = acc + __uint_as_float((uint32_t)s_acc[pr * kFew2Cols + col]) *
+            acc = acc + __uint_as_float((uint32_t)s_acc[pr * COLS + col]) *
                             s_prob[t * p.top_k + s];
         }
         p.out[(size_t)t * K + n0 + col] = (uint16_t)(f2bf_pk(acc, 0.0f) & 0xffffu);
@@ -579,18 +584,31 @@ hipError_t launch_few(const FewParams &p, hipStream_t stream) {
     int cap1 = (int)(kFewRowBytes / (p.K + 16));
     cap1 = cap1 < 1 ? 1 : cap1 > p.M ? p.M : cap1;
     const size_t lds1 = (size_t)cap1 * (p.K + 16);
-    hipLaunchKernelGGL(few_gmm1_kernel, dim3(p.I / (16 * kFew1Groups), most), dim3(kFewThreads), lds1,
-                       stream, p, cap1);
+    const dim3 grid1(p.I / (16 * kFew1Groups), most), block1(kFewThreads);
+    // the ring that loads fewer slices past a wave's share, the longer one where that is the same
+    // (K = 7168, one token: 39.2 us with 7 and 40.5 with 4; K = 4096, 5 tokens: 51 and 39)
+    const int share = (p.K / 64 + kFewWaves - 1) / kFewWaves;
+    if ((share + 6) / 7 * 7 <= (share + 3) / 4 * 4)
+        hipLaunchKernelGGL(few_gmm1_kernel<7>, grid1, block1, lds1, stream, p, cap1);
+    else
+        hipLaunchKernelGGL(few_gmm1_kernel<4>, grid1, block1, lds1, stream, p, cap1);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
+    // 32 columns to a workgroup (half as much quantising) where those fill most CUs
+    const int cols = p.K / 32 >= 192 ? 32 : 16;
     // beside the accumulators (at most 64 KB) two buffers of rows of at most 2048 elements: at
     // least 16 rows fit each, and no expert has more than M
-    const size_t acc = (size_t)R * kFew2Cols * 4;
+    const size_t acc = (size_t)R * cols * 4;
     const int i_cap = p.I < 2048 ? p.I : 2048;
     int cap2 = (int)((kFew2Bytes - acc) / 2 / (i_cap + 16));
     cap2 = cap2 > R ? R : cap2;
-    hipLaunchKernelGGL(few_gmm2_kernel, dim3(p.K / kFew2Cols), dim3(kFew2Threads),
-                       acc + (size_t)cap2 * 2 * (i_cap + 16), stream, p, cap2, i_cap);
+    const size_t lds2 = acc + (size_t)cap2 * 2 * (i_cap + 16);
+    if (cols == 32)
+        hipLaunchKernelGGL(few_gmm2_kernel<32>, dim3(p.K / 32), dim3(kFew2Threads), lds2, stream, p, cap2,
+                           i_cap);
+    else
+        hipLaunchKernelGGL(few_gmm2_kernel<16>, dim3(p.K / 16), dim3(kFew2Threads), lds2, stream, p, cap2,
+                           i_cap);
     return hipGetLastError();
 }
 

@@ -7,6 +7,8 @@
 // their scale byte.  GMM1 ends in SwiGLU: column n meets column N + n in the same
 // lane's accumulators, and silu(p[n]) * p[N + n] goes out as bf16; GMM2's p goes
 // out as fp16.
+#include <type_traits>
+
 #include "common.hpp"
 #include "dma.hpp"
 #include "kernels.hpp"
@@ -203,32 +205,51 @@ __device__ __forceinline__ void mx_short_scales(const MxGmmParams &p, const MxTi
     }
 }
 
-// The copies of stage s into slot `slot`: at every second stage SC of scales, then ac of rows and WC
-// of weight rows.  AC: ac where it is known (0: not).
+// The copies of stage s into slot `slot`: ac of rows, WC of weight rows, and at every second stage
+// SC of scales before them.  AC: ac where it is known (0: not).
+template <typename G, int AC>
+struct MxIssue {
+    static constexpr int N = (AC ? AC : G::AC) + G::WC;
+    const MxCopies<G> &c;
+    const uint8_t *ga, *gw;
+    uint32_t at;
+    int wave, ac;
+    __device__ __forceinline__ MxIssue(const MxGmmParams &p, const MxCopies<G> &c_, const MxLds &l, int s,
+                                       int slot)
+        : c(c_) {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        ac = AC ? AC : c.ac;
+        const int srow = p.Kred / 32;
+        if ((s & 1) == 0 && srow >= 16) {
+            const int start = mx_scale_start(s, srow);
+            const uint32_t to = l.scale_at + ((s >> 1) & 1) * G::SCALE;
+#pragma unroll
+            for (int i = 0; i < G::SC; ++i) {
+                const int k = mx_scale_copy<G>(i, wave);
+                const bool w = k < G::WR / 64;
+                dma16(uniform_ptr((w ? c.ws : p.a_scale) + start), c.soff[i],
+                      to + (w ? G::AR + 64 * k : 64 * k - G::WR) * 16);
+            }
+        }
+        at = l.data_at + slot * G::STAGE;
+        const int start = mx_start(s, 128, p.Kred / 2);
+        ga = uniform_ptr(p.a + start);
+        gw = uniform_ptr(c.wq + start);
+    }
+    __device__ __forceinline__ void copy(int i) const {  // 0 <= i < N
+        constexpr int A = AC ? AC : G::AC;
+        if (i >= A)
+            dma16(gw, c.voff_w[i - A], at + G::AR * 128 + (wave * G::WC + i - A) * 1024);
+        else if (AC || i < ac)
+            dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
+    }
+};
 template <typename G, int AC>
 __device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies<G> &c, const MxLds &l, int s,
                                          int slot) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int ac = AC ? AC : c.ac, srow = p.Kred / 32;
-    if ((s & 1) == 0 && srow >= 16) {
-        const int start = mx_scale_start(s, srow);
-        const uint32_t at = l.scale_at + ((s >> 1) & 1) * G::SCALE;
+    const MxIssue<G, AC> issue(p, c, l, s, slot);
 #pragma unroll
-        for (int i = 0; i < G::SC; ++i) {
-            const int k = mx_scale_copy<G>(i, wave);
-            const bool w = k < G::WR / 64;
-            dma16(uniform_ptr((w ? c.ws : p.a_scale) + start), c.soff[i],
-                  at + (w ? G::AR + 64 * k : 64 * k - G::WR) * 16);
-        }
-    }
-    const uint32_t at = l.data_at + slot * G::STAGE;
-    const int start = mx_start(s, 128, p.Kred / 2);
-    const uint8_t *ga = uniform_ptr(p.a + start), *gw = uniform_ptr(c.wq + start);
-#pragma unroll
-    for (int i = 0; i < (AC ? AC : G::AC); ++i)
-        if (AC || i < ac) dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < G::WC; ++i) dma16(gw, c.voff_w[i], at + G::AR * 128 + (wave * G::WC + i) * 1024);
+    for (int i = 0; i < issue.N; ++i) issue.copy(i);
 }
 
 // Reads of a stage in LDS: 32 rows from `row`, four fragments of 64 of the reduction and eight scale bytes.
@@ -308,7 +329,8 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     };
     // Two row fragments by two weight fragments: four sums that take turns, so that no product
     // waits for the one before it.  (With two, the loop ran at half the rate.)
-    auto multiply = [&](int pair, int first_half) {  // first_half: 0 or -1
+    // between(k) comes after the k-th of its 16 products.
+    auto multiply = [&](int pair, int first_half, auto between) {  // first_half: 0 or -1
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             asc[i][0] >>= 8 * g;  // the lane's blocks are g and 2 + g of each half
@@ -327,6 +349,7 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                     v16f &d = acc[2 * pair + i][j];
                     d = h & 1 ? mx_mfma32<1>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d)
                               : mx_mfma32<0>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d);
+                    between(4 * h + 2 * i + j);
                 }
         // the sums are wanted here: without this the compiler puts a stage's products together
         // behind its barrier and copies, where the reads no longer overlap them
@@ -343,10 +366,9 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         read_w(st, w, wsc);
         read_a(st, 0, a, asc);
     }
-#pragma unroll 1
-    for (int s = 0; s < ns; ++s) {
+    auto stage = [&](int s, auto copies) {  // copies: stage s + 2 is to be copied
         const MxStage<G> st(p, l, s, s & 1);
-        const int first_half = half && s + 1 == ns ? 0 : -1;
+        const int first_half = !copies.value && half && s + 1 == ns ? 0 : -1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             wsc[j][0] = wsc[j][0] >> (8 * g) & first_half;
@@ -367,22 +389,30 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
             read_a(st, pair + 1, na, nasc);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(pair, first_half);
+            multiply(pair, first_half, [](int) {});
             __builtin_amdgcn_sched_barrier(0);
             shift();
         }
         v4i nw[2][4] = {};
         int nwsc[2][2] = {};
-        if (s + 1 < ns) {
+        if (copies.value || s + 1 < ns) {
             wait_vmcnt<0>();  // stage s + 1
             __syncthreads();
-            if (s + 2 < ns) mx_issue<G, NP>(p, c, l, s + 2, s & 1);
             const MxStage<G> next(p, l, s + 1, (s + 1) & 1);
             read_w(next, nw, nwsc);
             read_a(next, 0, na, nasc);
         }
         __builtin_amdgcn_sched_barrier(0);
-        multiply(NP / 2 - 1, first_half);
+        if constexpr (copies.value) {  // one between two products: together they would hold them up
+            const MxIssue<G, NP> issue(p, c, l, s + 2, s & 1);
+            multiply(NP / 2 - 1, first_half, [&](int k) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (k < issue.N) issue.copy(k);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        } else {
+            multiply(NP / 2 - 1, first_half, [](int) {});
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -392,7 +422,11 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             wsc[j][1] = nwsc[j][1];
         }
         shift();
-    }
+    };
+#pragma unroll 1
+    for (int s = 0; s < ns - 2; ++s) stage(s, std::true_type{});
+#pragma unroll 1
+    for (int s = max(0, ns - 2); s < ns; ++s) stage(s, std::false_type{});
 
     if (more) {
         __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
