@@ -194,19 +194,19 @@ __device__ __forceinline__ int mx_scale_start(int s, int n) { return max(0, mx_s
 // pass the buffer's end, so they are read and written word by word, with the first stage.
 template <typename G>
 __device__ __forceinline__ void mx_short_scales(const MxGmmParams &p, const MxTile &t,
-                                                const MxCopies<G> &c, const MxLds &l) {
+                                                const MxCopies<G> &c, const MxLds &l, int sbuf) {
     const int srow = p.Kred / 32;
     if (srow >= 16) return;
     for (int r = threadIdx.x; r < G::AR + G::WR; r += kMxThreads) {
         const uint8_t *q = r < G::AR ? p.a_scale + (size_t)mx_data_row(p, t, l, r) * srow
                                      : c.ws + (size_t)mx_weight_row<G>(p, t, r - G::AR) * srow;
         for (int k = 0; k < srow; k += 4)
-            *reinterpret_cast<uint32_t *>(l.scale + r * 16 + k) = *reinterpret_cast<const uint32_t *>(q + k);
+            *reinterpret_cast<uint32_t *>(l.scale + sbuf * G::SCALE + r * 16 + k) = *reinterpret_cast<const uint32_t *>(q + k);
     }
 }
 
 // The copies of stage s into slot `slot`: ac of rows, WC of weight rows, and at every second stage
-// SC of scales before them.  AC: ac where it is known (0: not).
+// SC of scales before them, into scale buffer `sbuf`.  AC: ac where it is known (0: not).
 template <typename G, int AC>
 struct MxIssue {
     static constexpr int N = (AC ? AC : G::AC) + G::WC;
@@ -215,14 +215,14 @@ struct MxIssue {
     uint32_t at;
     int wave, ac;
     __device__ __forceinline__ MxIssue(const MxGmmParams &p, const MxCopies<G> &c_, const MxLds &l, int s,
-                                       int slot)
+                                       int slot, int sbuf)
         : c(c_) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         ac = AC ? AC : c.ac;
         const int srow = p.Kred / 32;
         if ((s & 1) == 0 && srow >= 16) {
             const int start = mx_scale_start(s, srow);
-            const uint32_t to = l.scale_at + ((s >> 1) & 1) * G::SCALE;
+            const uint32_t to = l.scale_at + sbuf * G::SCALE;
 #pragma unroll
             for (int i = 0; i < G::SC; ++i) {
                 const int k = mx_scale_copy<G>(i, wave);
@@ -246,8 +246,8 @@ struct MxIssue {
 };
 template <typename G, int AC>
 __device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies<G> &c, const MxLds &l, int s,
-                                         int slot) {
-    const MxIssue<G, AC> issue(p, c, l, s, slot);
+                                         int slot, int sbuf) {
+    const MxIssue<G, AC> issue(p, c, l, s, slot, sbuf);
 #pragma unroll
     for (int i = 0; i < issue.N; ++i) issue.copy(i);
 }
@@ -256,10 +256,10 @@ __device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies<G>
 template <typename G>
 struct MxStage {
     const uint8_t *q, *x;
-    __device__ __forceinline__ MxStage(const MxGmmParams &p, const MxLds &l, int s, int slot) {
+    __device__ __forceinline__ MxStage(const MxGmmParams &p, const MxLds &l, int s, int slot, int sbuf) {
         const int r = threadIdx.x & 31, srow = p.Kred / 32;
         q = l.data + slot * G::STAGE + r * 128;
-        x = l.scale + ((s >> 1) & 1) * G::SCALE + r * 16 + mx_start(s, 8, srow) - mx_scale_start(s, srow);
+        x = l.scale + sbuf * G::SCALE + r * 16 + mx_start(s, 8, srow) - mx_scale_start(s, srow);
     }
     __device__ __forceinline__ void read(int row, const int (&place)[4], v4i (&f)[4], int (&sc)[2]) const {
 #pragma unroll
@@ -286,8 +286,8 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // first fragments of stage s + 1 are read.
 //
 // The grid is persistent.  While a tile is multiplied the workgroup looks up its
-// next one, and the first two stages of that are copied while this one's sums
-// are rounded and stored.
+// next one, whose first two stages are copied in this one's last two, so that
+// they are there when its sums have been rounded and stored.
 constexpr int kMxList = 32;
 
 // One sum out of the accumulation registers.  (Left to the compiler, all 256 are copied
@@ -299,12 +299,13 @@ __device__ __forceinline__ float mx_sum(float a) {
 }
 
 // Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS and whose second is
-// under way, and rounds and stores its sums while the first stages of tile `nt` are copied.
+// under way, starts the copies of tile `nt`, and rounds and stores the sums.
 // (One body for every NP, with the rows behind conditions, made the compiler move the sums
 // between register files.)
 template <typename G, int NP>
 __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies<G> &c,
-                                        bool more, const MxTile &nt, const MxLds &l) {
+                                        bool more, const MxTile &nt, const MxLds &l, int &slot0,
+                                        int &sbuf0) {
     constexpr bool SWIGLU = G::SWIGLU;
     constexpr int F = SWIGLU ? 2 : 1;
     const int lane = threadIdx.x & (kWave - 1);
@@ -362,12 +363,18 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     // Each pair of fragments is read while the one before is multiplied; a stage's first pair and
     // weights while the stage before multiplies its last.
     {
-        const MxStage<G> st(p, l, 0, 0);
+        const MxStage<G> st(p, l, 0, slot0, sbuf0);
         read_w(st, w, wsc);
         read_a(st, 0, a, asc);
     }
+    // Slots and scale buffers go on from tile to tile.  With three stages or more the next tile's
+    // first two are copied in the last two of this one; else after it.
+    const bool stream = more && ns >= 3;
+    const int sbuf_next = (sbuf0 + (ns + 1) / 2) & 1;
+    auto slot = [&](int s) { return (slot0 + s) & 1; };
+    auto sbuf = [&](int s) { return (sbuf0 + (s >> 1)) & 1; };
     auto stage = [&](int s, auto copies) {  // copies: stage s + 2 is to be copied
-        const MxStage<G> st(p, l, s, s & 1);
+        const MxStage<G> st(p, l, s, slot(s), sbuf(s));
         const int first_half = !copies.value && half && s + 1 == ns ? 0 : -1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -398,19 +405,30 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         if (copies.value || s + 1 < ns) {
             wait_vmcnt<0>();  // stage s + 1
             __syncthreads();
-            const MxStage<G> next(p, l, s + 1, (s + 1) & 1);
+            const MxStage<G> next(p, l, s + 1, slot(s + 1), sbuf(s + 1));
             read_w(next, nw, nwsc);
             read_a(next, 0, na, nasc);
         }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (copies.value) {  // one between two products: together they would hold them up
-            const MxIssue<G, NP> issue(p, c, l, s + 2, s & 1);
+            const MxIssue<G, NP> issue(p, c, l, s + 2, slot(s), sbuf(s + 2));
             multiply(NP / 2 - 1, first_half, [&](int k) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (k < issue.N) issue.copy(k);
                 __builtin_amdgcn_sched_barrier(0);
             });
         } else {
+            if (stream) {  // the next tile's first stages instead
+                if (s + 2 == ns) {
+                    c = mx_copies<G>(p, nt, l, 2);
+                    mx_issue<G, 0>(p, c, l, 0, slot(s), sbuf_next);
+                } else {
+                    wait_vmcnt<0>();  // the first
+                    __syncthreads();
+                    mx_issue<G, 0>(p, c, l, 1, slot(s), sbuf_next);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
             multiply(NP / 2 - 1, first_half, [](int) {});
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -428,12 +446,15 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
 #pragma unroll 1
     for (int s = max(0, ns - 2); s < ns; ++s) stage(s, std::false_type{});
 
-    if (more) {
-        __syncthreads();  // every wave has read the last stage, and the next tile's routes are there
+    slot0 = slot(ns);
+    sbuf0 = sbuf_next;
+    if (more && !stream) {
+        wait_vmcnt<0>();  // the next tile's routes, which a reduction of one stage has not waited for
+        __syncthreads();  // and every wave has read the last stage
         c = mx_copies<G>(p, nt, l, 2);
-        mx_short_scales<G>(p, nt, c, l);
-        mx_issue<G, 0>(p, c, l, 0, 0);
-        if (ns > 1) mx_issue<G, 0>(p, c, l, 1, 1);
+        mx_short_scales<G>(p, nt, c, l, sbuf0);
+        mx_issue<G, 0>(p, c, l, 0, slot0, sbuf0);
+        if (ns > 1) mx_issue<G, 0>(p, c, l, 1, 1 - slot0, sbuf0);
     }
     // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
     // that each holds eight columns in a row and stores 16 bytes.
@@ -478,13 +499,8 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                     *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
             }
     }
-    if (more) {
-        // The first stage's copies are older than the second's, 10 at least, and than the stores:
-        // all but the last two fragments have whole rows, so at least that many were issued,
-        // unless columns past N were left out.
-        if (ns == 1) wait_vmcnt<0>();
-        else if (n0 + 64 / F <= p.N) wait_vmcnt<10 + (NP - 2) * J * 2>();
-        else wait_vmcnt<10>();
+    if (more && !stream) {
+        wait_vmcnt<0>();
         __syncthreads();
     }
 }
@@ -529,24 +545,25 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     wait_vmcnt<0>();
     __syncthreads();
     MxCopies<G> c = mx_copies<G>(p, cur, l, 2);
-    mx_short_scales<G>(p, cur, c, l);
-    mx_issue<G, 0>(p, c, l, 0, 0);
+    mx_short_scales<G>(p, cur, c, l, 0);
+    mx_issue<G, 0>(p, c, l, 0, 0, 0);
     if (p.Kred > 256) {
-        mx_issue<G, 0>(p, c, l, 1, 1);
-        wait_vmcnt<10>();
+        mx_issue<G, 0>(p, c, l, 1, 1, 0);
+        wait_vmcnt<10>();  // the second stage's copies are 10 at least
     } else {
         wait_vmcnt<0>();
     }
     __syncthreads();
+    int slot = 0, sbuf = 0;  // of the first stage of the tile
     for (int k = 1;; ++k) {
         const bool more = k < n;
         if (more && k % kMxList == 0) look_up(k);  // the last tiles of the list have been read
         const MxTile next = more ? mx_uniform(s_t[k % kMxList]) : cur;
         if (more) fetch_routes(next);
-        if (cur.rows > 192) mx_tile<G, 8>(p, cur, c, more, next, l);
-        else if (cur.rows > 128) mx_tile<G, 6>(p, cur, c, more, next, l);
-        else if (cur.rows > 64) mx_tile<G, 4>(p, cur, c, more, next, l);
-        else mx_tile<G, 2>(p, cur, c, more, next, l);
+        if (cur.rows > 192) mx_tile<G, 8>(p, cur, c, more, next, l, slot, sbuf);
+        else if (cur.rows > 128) mx_tile<G, 6>(p, cur, c, more, next, l, slot, sbuf);
+        else if (cur.rows > 64) mx_tile<G, 4>(p, cur, c, more, next, l, slot, sbuf);
+        else mx_tile<G, 2>(p, cur, c, more, next, l, slot, sbuf);
         if (!more) return;
         cur = next;
     }
@@ -576,8 +593,8 @@ __device__ __forceinline__ void mx_narrow(const MxGmmParams &p, const MxTile &t,
         else wait_vmcnt<0>();
         __syncthreads();  // and every wave has read stage s - 1, whose slot is the next
         const int free = slot == 0 ? 2 : slot - 1;
-        if (s + 2 < ns) mx_issue<G, NP>(p, c, l, s + 2, free);
-        const MxStage<G> st(p, l, s, slot);
+        if (s + 2 < ns) mx_issue<G, NP>(p, c, l, s + 2, free, ((s >> 1) + 1) & 1);
+        const MxStage<G> st(p, l, s, slot, (s >> 1) & 1);
         v4i w[4], a[NP][4];
         int wsc[2], asc[NP][2];
         st.read(G::AR + wave * 32, place, w, wsc);
@@ -660,9 +677,9 @@ mxfp4_gmm_narrow_kernel(MxGmmParams p) {
     if (p.a_route && tid < G::AR) s_route[tid] = p.a_route[tile.row0 + min(tid, tile.rows - 1)];
     __syncthreads();
     const MxCopies<G> c = mx_copies<G>(p, tile, l, 1);
-    mx_short_scales<G>(p, tile, c, l);
-    mx_issue<G, 0>(p, c, l, 0, 0);
-    if (p.Kred > 256) mx_issue<G, 0>(p, c, l, 1, 1);
+    mx_short_scales<G>(p, tile, c, l, 0);
+    mx_issue<G, 0>(p, c, l, 0, 0, 0);
+    if (p.Kred > 256) mx_issue<G, 0>(p, c, l, 1, 1, 0);
     if (tile.rows > 32) mx_narrow<G, 2>(p, tile, c, l);
     else mx_narrow<G, 1>(p, tile, c, l);
 }

@@ -415,6 +415,31 @@ def test_gmm(first, case):
     assert same_bits(y, run_gmm(first, d, a, asc, route, cumsum, w, wsc)), "two calls differ"
 
 
+def check_gmm(first, counts, M, K, top_k, I, seed):
+    d, (a, asc), route, cumsum, (w, wsc) = gmm_inputs(first, counts, M, K, top_k, I, seed=seed)
+    y = run_gmm(first, d, a, asc, route, cumsum, w, wsc)
+    ref, tol = gmm_reference(first, a, asc, route, cumsum, w, wsc, top_k)
+    n = sum(counts)
+    ref.sub_(y.double()).abs_()
+    assert (ref[:n] <= tol[:n]).all()
+    assert (y[n:] == -7).all()
+
+
+# A persistent workgroup's second tile and those after it: of every number of stages from one to
+# six, whole and half ones, and of different heights.
+@pytest.mark.parametrize("first", [True, False], ids=["gmm1", "gmm2"])
+@pytest.mark.parametrize("reduction", [128, 256, 384, 512, 640, 768, 1024, 1152, 1536])
+def test_gmm_several_tiles_a_workgroup(first, reduction):
+    K, I = (reduction, 8192) if first else (16384, reduction)
+    check_gmm(first, [300, 0, 520, 70, 0, 513, 900, 257], 1300, K, 2, I, seed=reduction)
+
+
+@pytest.mark.parametrize("K", [128, 768])
+def test_gmm_long_tile_lists(K):
+    """More tiles to a workgroup than it looks up at once."""
+    check_gmm(True, [65] * 72, 2400, K, 2, 16384, seed=K)
+
+
 @pytest.mark.parametrize("first", [True, False], ids=["gmm1", "gmm2"])
 @pytest.mark.parametrize("counts,M", [([2, 0, 3], 4), ([40, 0, 30], 40), ([300, 0, 200], 300)])
 def test_gmm_nan_stays_where_it_is(first, counts, M):
