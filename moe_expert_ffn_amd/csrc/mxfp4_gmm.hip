@@ -59,9 +59,9 @@ __device__ __forceinline__ v16f mx_mfma32(v4i w, int ws, v4i a, int as, v16f acc
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, a8, acc, 4, 4, 2 * H, ws, 2 * H, as);
 }
 
-// 16-byte chunk c of a 128-byte row: the place without bank conflicts for reads of
-// one chunk index of consecutive rows
-__device__ __forceinline__ int mx_swz(int row, int c) { return c ^ (row & 7); }
+// 16-byte chunk c of a 128-byte row: its place.  LDS has 64 banks, two rows; reads of one chunk
+// index of 16 rows in the order of the lanes meet each bank once.
+__device__ __forceinline__ int mx_swz(int row, int c) { return c ^ (row >> 1 & 7); }
 
 // The tiles, numbered by expert, weight block and row block; an expert's rows are
 // split evenly over its row blocks in units of 32.
@@ -205,51 +205,66 @@ __device__ __forceinline__ void mx_short_scales(const MxGmmParams &p, const MxTi
     }
 }
 
-// The copies of stage s into slot `slot`: ac of rows, WC of weight rows, and at every second stage
-// SC of scales before them, into scale buffer `sbuf`.  AC: ac where it is known (0: not).
-template <typename G, int AC>
-struct MxIssue {
-    static constexpr int N = (AC ? AC : G::AC) + G::WC;
+// The copies of stage s into slot `slot`, and of scales, with every second stage, into scale buffer
+// `sbuf`: WC + SC of weight rows and scales, ac of rows.
+template <typename G>
+struct MxIssueW {
+    static constexpr int N = G::WC + G::SC;
     const MxCopies<G> &c;
-    const uint8_t *ga, *gw;
-    uint32_t at;
-    int wave, ac;
-    __device__ __forceinline__ MxIssue(const MxGmmParams &p, const MxCopies<G> &c_, const MxLds &l, int s,
-                                       int slot, int sbuf)
+    const uint8_t *gw, *gs, *ga;
+    uint32_t at, scale_at;
+    int wave;
+    bool scales;
+    __device__ __forceinline__ MxIssueW(const MxGmmParams &p, const MxCopies<G> &c_, const MxLds &l, int s,
+                                        int slot, int sbuf)
         : c(c_) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        ac = AC ? AC : c.ac;
-        const int srow = p.Kred / 32;
-        if ((s & 1) == 0 && srow >= 16) {
-            const int start = mx_scale_start(s, srow);
-            const uint32_t to = l.scale_at + sbuf * G::SCALE;
-#pragma unroll
-            for (int i = 0; i < G::SC; ++i) {
-                const int k = mx_scale_copy<G>(i, wave);
-                const bool w = k < G::WR / 64;
-                dma16(uniform_ptr((w ? c.ws : p.a_scale) + start), c.soff[i],
-                      to + (w ? G::AR + 64 * k : 64 * k - G::WR) * 16);
-            }
-        }
-        at = l.data_at + slot * G::STAGE;
-        const int start = mx_start(s, 128, p.Kred / 2);
-        ga = uniform_ptr(p.a + start);
-        gw = uniform_ptr(c.wq + start);
+        const int srow = p.Kred / 32, start = mx_scale_start(s, srow);
+        scales = (s & 1) == 0 && srow >= 16;
+        gs = uniform_ptr(c.ws + start);
+        ga = uniform_ptr(p.a_scale + start);
+        scale_at = l.scale_at + sbuf * G::SCALE;
+        gw = uniform_ptr(c.wq + mx_start(s, 128, p.Kred / 2));
+        at = l.data_at + slot * G::STAGE + G::AR * 128 + wave * G::WC * 1024;
     }
     __device__ __forceinline__ void copy(int i) const {  // 0 <= i < N
-        constexpr int A = AC ? AC : G::AC;
-        if (i >= A)
-            dma16(gw, c.voff_w[i - A], at + G::AR * 128 + (wave * G::WC + i - A) * 1024);
-        else if (AC || i < ac)
-            dma16(ga, c.voff_a[i], at + (wave * ac + i) * 1024);
+        if (i < G::WC) {
+            dma16(gw, c.voff_w[i], at + i * 1024);
+        } else if (scales) {
+            const int k = mx_scale_copy<G>(i - G::WC, wave);
+            const bool w = k < G::WR / 64;
+            dma16(uniform_ptr(w ? gs : ga), c.soff[i - G::WC], scale_at + (w ? G::AR + 64 * k : 64 * k - G::WR) * 16);
+        }
     }
 };
+template <typename G, int AC>  // AC: ac where it is known (0: not)
+struct MxIssueA {
+    static constexpr int N = AC ? AC : G::AC;
+    const MxCopies<G> &c;
+    const uint8_t *ga;
+    uint32_t at;
+    int ac;
+    __device__ __forceinline__ MxIssueA(const MxGmmParams &p, const MxCopies<G> &c_, const MxLds &l, int s,
+                                        int slot)
+        : c(c_) {
+        ac = AC ? AC : c.ac;
+        ga = uniform_ptr(p.a + mx_start(s, 128, p.Kred / 2));
+        at = l.data_at + slot * G::STAGE + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * ac * 1024;
+    }
+    __device__ __forceinline__ void copy(int i) const {  // 0 <= i < N
+        if (AC || i < ac) dma16(ga, c.voff_a[i], at + i * 1024);
+    }
+};
+template <typename I>
+__device__ __forceinline__ void mx_all(const I &issue, int from = 0, int to = I::N) {
+#pragma unroll
+    for (int i = from; i < to; ++i) issue.copy(i);
+}
 template <typename G, int AC>
 __device__ __forceinline__ void mx_issue(const MxGmmParams &p, const MxCopies<G> &c, const MxLds &l, int s,
                                          int slot, int sbuf) {
-    const MxIssue<G, AC> issue(p, c, l, s, slot, sbuf);
-#pragma unroll
-    for (int i = 0; i < issue.N; ++i) issue.copy(i);
+    mx_all(MxIssueW<G>(p, c, l, s, slot, sbuf));
+    mx_all(MxIssueA<G, AC>(p, c, l, s, slot));
 }
 
 // Reads of a stage in LDS: 32 rows from `row`, four fragments of 64 of the reduction and eight scale bytes.
@@ -280,10 +295,12 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // tile follows its live rows in steps of 64 and no wave idles in a ragged one; 8 x 2
 // fragments of 32 x 32 sums fill half of the register file.
 //
-// The stages alternate between two slots.  The barrier between stages s and s + 1 lies
-// before the last rows of stage s are multiplied: those are in registers by then,
-// so behind it the copies of stage s + 2 start, into the slot of stage s, and the
-// first fragments of stage s + 1 are read.
+// The stages alternate between two slots.  A wave multiplies by weight rows that it has
+// copied itself, and has all of a stage's in registers when the stage begins: the
+// weights of stage s + 2 are copied from then on, and have nearly two stages to come from
+// memory.  The barrier between stages s and s + 1 lies before the last rows of stage s
+// are multiplied: those are in registers by then, so behind it the rows of stage s + 2 are
+// copied, and the first fragments of stage s + 1 are read.
 //
 // The grid is persistent.  While a tile is multiplied the workgroup looks up its
 // next one, whose first two stages are copied in this one's last two, so that
@@ -299,17 +316,19 @@ __device__ __forceinline__ float mx_sum(float a) {
 }
 
 // Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS and whose second is
-// under way, starts the copies of tile `nt`, and rounds and stores the sums.
+// under way, starts the copies of tile `nt`, and rounds and stores the sums.  `stores`: at least
+// 4 J times as many stores of the tile before have been made since its copies.
 // (One body for every NP, with the rows behind conditions, made the compiler move the sums
 // between register files.)
 template <typename G, int NP>
 __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, MxCopies<G> &c,
                                         bool more, const MxTile &nt, const MxLds &l, int &slot0,
-                                        int &sbuf0) {
+                                        int &sbuf0, int &stores) {
     constexpr bool SWIGLU = G::SWIGLU;
     constexpr int F = SWIGLU ? 2 : 1;
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int J = 2 / F;  // column fragments of 32 that a wave stores
     const int ns = (p.Kred + 255) / 256;
     const bool half = p.Kred % 256 != 0;  // of the last stage's row pieces the second halves alone
 
@@ -367,15 +386,37 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
         read_w(st, w, wsc);
         read_a(st, 0, a, asc);
     }
-    // Slots and scale buffers go on from tile to tile.  With three stages or more the next tile's
-    // first two are copied in the last two of this one; else after it.
-    const bool stream = more && ns >= 3;
+    // Slots and scale buffers go on from tile to tile.  With four stages or more the next tile's
+    // first two are copied in the last two of this one (its routes, asked for before this tile, are
+    // there after the second stage's barrier); else after it.
+    const bool stream = more && ns >= 4;
     const int sbuf_next = (sbuf0 + (ns + 1) / 2) & 1;
     auto slot = [&](int s) { return (slot0 + s) & 1; };
     auto sbuf = [&](int s) { return (sbuf0 + (s >> 1)) & 1; };
+    // Waits for all but the newest NEWER of the wave's copies; in the first stage, whose copies are
+    // older than the last tile's stores, not for those either.
+    auto wait_copies = [&](int s, auto newer) {
+        constexpr int NEWER = newer.value, U = 4 * J;
+        if (s > 0 || stores == 0) wait_vmcnt<NEWER>();
+        else if (stores == 1) wait_vmcnt<NEWER + U>();
+        else if (stores == 2) wait_vmcnt<NEWER + 2 * U>();
+        else wait_vmcnt<NEWER + 3 * U>();
+    };
+    typedef std::integral_constant<int, 0> None;
+    typedef std::integral_constant<int, G::WC> Weights;
+    typedef std::integral_constant<int, G::WC + G::SC> WeightsScales;
     auto stage = [&](int s, auto copies) {  // copies: stage s + 2 is to be copied
         const MxStage<G> st(p, l, s, slot(s), sbuf(s));
         const int first_half = !copies.value && half && s + 1 == ns ? 0 : -1;
+        // the stage's weights are in registers, and their place is free
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const MxIssueW<G> issue_w(p, c, l, s + 2, slot(s), sbuf(s + 2));
+        if constexpr (copies.value) {
+            if (NP == 2) mx_all(issue_w);
+        } else if (stream) {  // the next tile's first stages instead
+            if (s + 2 == ns) c = mx_copies<G>(p, nt, l, 2);
+            mx_all(MxIssueW<G>(p, c, l, s + 2 - ns, slot(s), sbuf_next), 0, G::WC);
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             wsc[j][0] = wsc[j][0] >> (8 * g) & first_half;
@@ -392,43 +433,52 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                 asc[i][1] = nasc[i][1];
             }
         };
+        // one copy between two products: together they would hold them up
+        auto between = [&](const auto &issue) {
+            return [&](int k) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (k < issue.N) issue.copy(k);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+        };
 #pragma unroll
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
             read_a(st, pair + 1, na, nasc);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(pair, first_half, [](int) {});
+            if constexpr (copies.value) {
+                if (pair == 0) multiply(pair, first_half, between(issue_w));
+                else multiply(pair, first_half, [](int) {});
+            } else {
+                multiply(pair, first_half, [](int) {});
+            }
             __builtin_amdgcn_sched_barrier(0);
             shift();
         }
         v4i nw[2][4] = {};
         int nwsc[2][2] = {};
-        if (copies.value || s + 1 < ns) {
-            wait_vmcnt<0>();  // stage s + 1
+        if (copies.value || s + 1 < ns || stream) {
+            // stage s + 1 (of the tiles together)
+            if (copies.value && issue_w.scales) wait_copies(s, WeightsScales{});
+            else if (copies.value || stream) wait_copies(s, Weights{});
+            else wait_copies(s, None{});
             __syncthreads();
-            const MxStage<G> next(p, l, s + 1, slot(s + 1), sbuf(s + 1));
-            read_w(next, nw, nwsc);
-            read_a(next, 0, na, nasc);
+            if (copies.value || s + 1 < ns) {
+                const MxStage<G> next(p, l, s + 1, slot(s + 1), sbuf(s + 1));
+                read_w(next, nw, nwsc);
+                read_a(next, 0, na, nasc);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (copies.value) {  // one between two products: together they would hold them up
-            const MxIssue<G, NP> issue(p, c, l, s + 2, slot(s), sbuf(s + 2));
-            multiply(NP / 2 - 1, first_half, [&](int k) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (k < issue.N) issue.copy(k);
-                __builtin_amdgcn_sched_barrier(0);
-            });
+        if constexpr (copies.value) {
+            const MxIssueA<G, NP> issue(p, c, l, s + 2, slot(s));
+            multiply(NP / 2 - 1, first_half, between(issue));
         } else {
-            if (stream) {  // the next tile's first stages instead
-                if (s + 2 == ns) {
-                    c = mx_copies<G>(p, nt, l, 2);
-                    mx_issue<G, 0>(p, c, l, 0, slot(s), sbuf_next);
-                } else {
-                    wait_vmcnt<0>();  // the first
-                    __syncthreads();
-                    mx_issue<G, 0>(p, c, l, 1, slot(s), sbuf_next);
-                }
-                __builtin_amdgcn_sched_barrier(0);
+            if (stream) {
+                // its scales here, as their buffer may be the one that stage ns - 2 has read
+                mx_all(MxIssueW<G>(p, c, l, s + 2 - ns, slot(s), sbuf_next), G::WC);
+                mx_all(MxIssueA<G, 0>(p, c, l, s + 2 - ns, slot(s)));
             }
+            __builtin_amdgcn_sched_barrier(0);
             multiply(NP / 2 - 1, first_half, [](int) {});
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -458,7 +508,6 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     }
     // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
     // that each holds eight columns in a row and stores 16 bytes.
-    constexpr int J = 2 / F;
     uint2 out[NP][J][4];
     // the last product's result is there after 18 wait states
     asm volatile("s_nop 15\n\ts_nop 15");
@@ -499,8 +548,17 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                     *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
             }
     }
-    if (more && !stream) {
-        wait_vmcnt<0>();
+    // all but the last two fragments have whole rows: so many stores were made at least
+    stores = n0 + 64 / F <= p.N ? NP / 2 - 1 : 0;
+    if (more && !stream) {  // the next tile's first stage: the second's copies, 10 at least, are newer
+        if (ns == 1) {
+            wait_vmcnt<0>();
+            stores = 0;
+        } else if (stores) {
+            wait_vmcnt<10 + (NP - 2) * J * 2>();
+        } else {
+            wait_vmcnt<10>();
+        }
         __syncthreads();
     }
 }
@@ -555,15 +613,16 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     }
     __syncthreads();
     int slot = 0, sbuf = 0;  // of the first stage of the tile
+    int stores = 0;          // see mx_tile
     for (int k = 1;; ++k) {
         const bool more = k < n;
         if (more && k % kMxList == 0) look_up(k);  // the last tiles of the list have been read
         const MxTile next = more ? mx_uniform(s_t[k % kMxList]) : cur;
         if (more) fetch_routes(next);
-        if (cur.rows > 192) mx_tile<G, 8>(p, cur, c, more, next, l, slot, sbuf);
-        else if (cur.rows > 128) mx_tile<G, 6>(p, cur, c, more, next, l, slot, sbuf);
-        else if (cur.rows > 64) mx_tile<G, 4>(p, cur, c, more, next, l, slot, sbuf);
-        else mx_tile<G, 2>(p, cur, c, more, next, l, slot, sbuf);
+        if (cur.rows > 192) mx_tile<G, 8>(p, cur, c, more, next, l, slot, sbuf, stores);
+        else if (cur.rows > 128) mx_tile<G, 6>(p, cur, c, more, next, l, slot, sbuf, stores);
+        else if (cur.rows > 64) mx_tile<G, 4>(p, cur, c, more, next, l, slot, sbuf, stores);
+        else mx_tile<G, 2>(p, cur, c, more, next, l, slot, sbuf, stores);
         if (!more) return;
         cur = next;
     }
