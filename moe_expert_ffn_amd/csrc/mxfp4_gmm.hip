@@ -276,11 +276,22 @@ struct MxStage {
         q = l.data + slot * G::STAGE + r * 128;
         x = l.scale + sbuf * G::SCALE + r * 16 + mx_start(s, 8, srow) - mx_scale_start(s, srow);
     }
-    __device__ __forceinline__ void read(int row, const int (&place)[4], v4i (&f)[4], int (&sc)[2]) const {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) f[h] = *reinterpret_cast<const v4i *>(q + row * 128 + place[h]);
+    __device__ __forceinline__ void codes(int row, int place, v4i &f) const {
+        f = *reinterpret_cast<const v4i *>(q + row * 128 + place);
+    }
+    __device__ __forceinline__ void scales(int row, int (&sc)[2]) const {
         sc[0] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16);
         sc[1] = (int)*reinterpret_cast<const uint32_t *>(x + row * 16 + 4);
+    }
+    __device__ __forceinline__ void read(int row, const int (&place)[4], v4i (&f)[4], int (&sc)[2]) const {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) codes(row, place[h], f[h]);
+        scales(row, sc);
+    }
+    // the same for two times 32 rows in ten steps, in the order in which products want them
+    __device__ __forceinline__ void step(int k, int row, const int (&place)[4], v4i (&f)[2][4], int (&sc)[2][2]) const {
+        if (k < 2) scales(row + 32 * k, sc[k]);
+        else codes(row + 32 * (k & 1), place[k / 2 - 1], f[k & 1][k / 2 - 1]);
     }
 };
 
@@ -336,20 +347,14 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     int place[4];  // of the lane in a row of a stage, 64 of the reduction each
 #pragma unroll
     for (int h = 0; h < 4; ++h) place[h] = mx_swz(r, 2 * h + g) * 16;
-    auto read_w = [&](const MxStage<G> &st, v4i (&f)[2][4], int (&sc)[2][2]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) st.read(G::AR + wave * 64 + 32 * j, place, f[j], sc[j]);
-    };
+    const int wrow = G::AR + wave * 64;
     v16f acc[NP][2] = {};
     v4i w[2][4], a[2][4];  // weights of the stage, rows of the two fragments that are multiplied
     int wsc[2][2], asc[2][2];
-    auto read_a = [&](const MxStage<G> &st, int pair, v4i (&f)[2][4], int (&sc)[2][2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) st.read(64 * pair + 32 * i, place, f[i], sc[i]);
-    };
     // Two row fragments by two weight fragments: four sums that take turns, so that no product
     // waits for the one before it.  (With two, the loop ran at half the rate.)
-    // between(k) comes after the k-th of its 16 products.
+    // between(k) comes after the k-th of its 16 products: reads and copies there, one or two at a
+    // time, as a batch of either held the products up while it was taken in.
     auto multiply = [&](int pair, int first_half, auto between) {  // first_half: 0 or -1
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -369,7 +374,9 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                     v16f &d = acc[2 * pair + i][j];
                     d = h & 1 ? mx_mfma32<1>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d)
                               : mx_mfma32<0>(w[j][h], wsc[j][h >> 1], a[i][h], asc[i][h >> 1], d);
+                    __builtin_amdgcn_sched_barrier(0);
                     between(4 * h + 2 * i + j);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
         // the sums are wanted here: without this the compiler puts a stage's products together
         // behind its barrier and copies, where the reads no longer overlap them
@@ -383,8 +390,11 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     // weights while the stage before multiplies its last.
     {
         const MxStage<G> st(p, l, 0, slot0, sbuf0);
-        read_w(st, w, wsc);
-        read_a(st, 0, a, asc);
+#pragma unroll
+        for (int k = 0; k < 10; ++k) {
+            st.step(k, wrow, place, w, wsc);
+            st.step(k, 0, place, a, asc);
+        }
     }
     // Slots and scale buffers go on from tile to tile.  With four stages or more the next tile's
     // first two are copied in the last two of this one (its routes, asked for before this tile, are
@@ -422,8 +432,8 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             wsc[j][0] = wsc[j][0] >> (8 * g) & first_half;
             wsc[j][1] >>= 8 * g;
         }
-        v4i na[2][4];
-        int nasc[2][2];
+        v4i na[2][4] = {};
+        int nasc[2][2] = {};
         auto shift = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -433,25 +443,13 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
                 asc[i][1] = nasc[i][1];
             }
         };
-        // one copy between two products: together they would hold them up
-        auto between = [&](const auto &issue) {
-            return [&](int k) {
-                __builtin_amdgcn_sched_barrier(0);
-                if (k < issue.N) issue.copy(k);
-                __builtin_amdgcn_sched_barrier(0);
-            };
-        };
 #pragma unroll
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
-            read_a(st, pair + 1, na, nasc);
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (copies.value) {
-                if (pair == 0) multiply(pair, first_half, between(issue_w));
-                else multiply(pair, first_half, [](int) {});
-            } else {
-                multiply(pair, first_half, [](int) {});
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            multiply(pair, first_half, [&](int k) {
+                if (k < 10) st.step(k, 64 * (pair + 1), place, na, nasc);
+                if constexpr (copies.value)
+                    if (pair == 0 && k < issue_w.N) issue_w.copy(k);
+            });
             shift();
         }
         v4i nw[2][4] = {};
@@ -462,24 +460,27 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             else if (copies.value || stream) wait_copies(s, Weights{});
             else wait_copies(s, None{});
             __syncthreads();
-            if (copies.value || s + 1 < ns) {
-                const MxStage<G> next(p, l, s + 1, slot(s + 1), sbuf(s + 1));
-                read_w(next, nw, nwsc);
-                read_a(next, 0, na, nasc);
-            }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        const MxStage<G> next(p, l, min(s + 1, ns - 1), slot(s + 1), sbuf(s + 1));
+        auto read_next = [&](int k) {
+            if (k < 10) {
+                next.step(k, wrow, place, nw, nwsc);
+                next.step(k, 0, place, na, nasc);
+            }
+        };
         if constexpr (copies.value) {
             const MxIssueA<G, NP> issue(p, c, l, s + 2, slot(s));
-            multiply(NP / 2 - 1, first_half, between(issue));
+            multiply(NP / 2 - 1, first_half, [&](int k) {
+                read_next(k);
+                if (k >= 16 - issue.N) issue.copy(k - (16 - issue.N));
+            });
         } else {
             if (stream) {
                 // its scales here, as their buffer may be the one that stage ns - 2 has read
                 mx_all(MxIssueW<G>(p, c, l, s + 2 - ns, slot(s), sbuf_next), G::WC);
                 mx_all(MxIssueA<G, 0>(p, c, l, s + 2 - ns, slot(s)));
             }
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(NP / 2 - 1, first_half, [](int) {});
+            multiply(NP / 2 - 1, first_half, read_next);  // in the last stage nobody looks at what it reads
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
