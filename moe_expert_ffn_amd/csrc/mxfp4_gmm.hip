@@ -448,8 +448,11 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
             multiply(pair, first_half, [&](int k) {
                 if (k < 10) st.step(k, 64 * (pair + 1), place, na, nasc);
                 if constexpr (copies.value)
-                    if (pair == 0 && k < issue_w.N) issue_w.copy(k);
+                    if (pair == 0 && k < G::WC) issue_w.copy(k);
             });
+            // not between products: the compiler moves products down past a branch
+            if constexpr (copies.value)
+                if (pair == 0) mx_all(issue_w, G::WC);
             shift();
         }
         v4i nw[2][4] = {};
