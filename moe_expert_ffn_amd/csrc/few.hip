@@ -16,9 +16,9 @@
 //    gate columns at a time with the reduction split over its waves (an exact
 //    integer sum), and writes y = silu * gate in fp32 with the largest |y| of
 //    its columns.
-//  * few_gmm2_kernel, one workgroup per 32 output columns: quantises every
+//  * few_gmm2_kernel, one workgroup per 32 or 16 output columns: quantises every
 //    pair's y into LDS (the row maximum is that of the 16-column maxima),
-//    multiplies each expert's rows by its 32 columns, and combines the slots of
+//    multiplies each expert's rows by its columns, and combines the slots of
 //    every token in order, so no partial result leaves the workgroup.
 // A wave reads weights straight from memory into fragments: 16 columns of one
 // 64-byte K slice are 1 KB in a row in the packed layout.
@@ -122,6 +122,8 @@ __device__ __forceinline__ v4i few_mfma(v4i w, v4i a, v4i acc) {
 }
 
 // ---------------------------------------------------------------------------
+// K = 7168, I = 2048, E = 32, top_k = 8: 38 us at one token and 152 at 16, of 35 and 140 for
+// the weights alone at 6.7 TB/s.
 constexpr int kFew1Groups = 2;  // groups of 16 columns that share the quantised rows
 
 template <int U>  // K slices a wave has in flight

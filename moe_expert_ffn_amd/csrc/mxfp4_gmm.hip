@@ -3,7 +3,7 @@
 //
 // For every row of expert e's group, p[n] = sum_k a[k] * w[e][n][k] over the
 // values that codes and block scales stand for, in fp32 on the matrix cores:
-// v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 codes of a lane (one block) with
+// v_mfma_scale_f32_32x32x64_f8f6f4 takes 32 codes of a lane (one block) with
 // their scale byte.  GMM1 ends in SwiGLU: column n meets column N + n in the same
 // lane's accumulators, and silu(p[n]) * p[N + n] goes out as bf16; GMM2's p goes
 // out as fp16.
@@ -312,6 +312,14 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // memory.  The barrier between stages s and s + 1 lies before the last rows of stage s
 // are multiplied: those are in registers by then, so behind it the rows of stage s + 2 are
 // copied, and the first fragments of stage s + 1 are read.
+//
+// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 302 us, 3.2 PFLOP/s of the 6.5
+// above, gmm2 192; 512 tokens: 110 and 78.  Copies and reads without products take
+// nine tenths of that and products without copies eight, so neither hides the other
+// altogether, and with operands of zero the same work takes three quarters of the time:
+// the card lowers its clock under it.  Words of later stages fetched ahead into the
+// L2, non-temporal stores (gmm2 of 4096 tokens 176 -> 235 us) and 64-byte
+// pieces of a row to a store gave nothing or less.
 //
 // The grid is persistent.  While a tile is multiplied the workgroup looks up its
 // next one, whose first two stages are copied in this one's last two, so that
@@ -636,7 +644,8 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
 // Few rows per expert: the product streams weights.  Tiles of at most 64 rows by 128
 // weight rows; two workgroups fit a CU, so that one copies while the other looks up its tile,
 // waits for its first stage or stores.  Three slots: two stages are under way while one is
-// multiplied.
+// multiplied.  At the sizes above one token takes 21 us and 12 (weights of its eight
+// experts at 5.8 TB/s), 128 tokens 95 and 57 (5.3).
 template <typename G, int NP>
 __device__ __forceinline__ void mx_narrow(const MxGmmParams &p, const MxTile &t, const MxCopies<G> &c,
                                           const MxLds &l) {

@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmegamoe.so")
 
 MEGAMOE_OK = 0
+MEGAMOE_EUNSUPPORTED = 2  # dims outside the limits
 MEGAMOE_EDEVICE = 5  # megamoe_last_error: routes were dropped
 
 
@@ -366,6 +367,13 @@ def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, str
     _launch("megamoe_route", (logits, bias, expert_idx, probs), args, stream)
 
 
+def _packed(name: str, w: torch.Tensor, d, k: int, n: int) -> None:
+    """Packed weights of E experts' k by n: columns in whole blocks of 256."""
+    need = d.E * k * ((n + 255) // 256 * 256)
+    if w.numel() < need:
+        raise ValueError(f"{name}: expected at least {need} elements, got {w.numel()}")
+
+
 def megamoe_few_workspace_bytes(d: megamoe_dims) -> int:
     n = ctypes.c_size_t(0)
     _check("megamoe_few_workspace_bytes",
@@ -378,6 +386,10 @@ def megamoe_forward_few(d, x, expert_idx, probs, w1p, scale1, w2p, scale2, out, 
     _shape("x", x, d.M, d.K)
     _shape("expert_idx", expert_idx, d.M, d.top_k)
     _shape("probs", probs, d.M, d.top_k)
+    _packed("w1p", w1p, d, d.K, 2 * d.I)
+    _shape("scale1", scale1, d.E, 2 * d.I)
+    _packed("w2p", w2p, d, d.I, d.K)
+    _shape("scale2", scale2, d.E, d.K)
     _shape("out", out, d.M, d.K)
     args = (ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
             _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
@@ -486,6 +498,11 @@ class MegaMoE:
         self.device = torch.device(device)
         self.workspace = torch.empty(megamoe_workspace_bytes(self.d), dtype=torch.uint8,
                                      device=self.device)
+        self.few_workspace = None  # where the dims allow forward_few
+        if M <= 16 and M * top_k <= 512:
+            self.few_workspace = torch.empty(megamoe_few_workspace_bytes(self.d),
+                                             dtype=torch.uint8, device=self.device)
+        self._last = self.workspace
         n1, n2 = megamoe_packed_weight_bytes(self.d)
         self.w1p = torch.empty(n1, dtype=torch.int8, device=self.device)
         self.w2p = torch.empty(n2, dtype=torch.int8, device=self.device)
@@ -498,12 +515,76 @@ class MegaMoE:
         self.scale1 = scale1.contiguous()
         self.scale2 = scale2.contiguous()
 
+    def route(self, logits, bias=None, renormalize=True):
+        """Router logits [M, E] -> expert_idx and probs for forward and forward_few."""
+        return _route(self.d, logits, bias, renormalize)
+
     def forward(self, x, expert_idx, probs, out=None):
         if out is None:
             out = torch.empty((self.d.M, self.d.K), dtype=torch.bfloat16, device=self.device)
         megamoe_forward(self.d, x, expert_idx, probs, self.w1p, self.scale1, self.w2p,
                         self.scale2, out, self.workspace)
+        self._last = self.workspace
+        return out
+
+    def forward_few(self, x, expert_idx, probs, out=None):
+        """forward in two kernels, for M <= 16: the same result, sooner for the smallest batches."""
+        if self.few_workspace is None:
+            raise MegaMoEError("megamoe_forward_few", MEGAMOE_EUNSUPPORTED)
+        if out is None:
+            out = torch.empty((self.d.M, self.d.K), dtype=torch.bfloat16, device=self.device)
+        megamoe_forward_few(self.d, x, expert_idx, probs, self.w1p, self.scale1, self.w2p,
+                            self.scale2, out, self.few_workspace)
+        self._last = self.few_workspace
         return out
 
     def last_error(self) -> int:
+        """Routes that the last forward dropped."""
+        return megamoe_last_error(self._last)
+
+
+class MegaMoEMXFP4:
+    """Convenience holder: MXFP4 weights + workspace for one set of dims."""
+
+    def __init__(self, M: int, K: int, E: int, top_k: int, I: int, device="cuda"):
+        self.d = dims(M, K, E, top_k, I)
+        _check("megamoe_check_dims", megamoe_check_dims(self.d))
+        self.device = torch.device(device)
+
+        def empty(*shape):
+            return torch.empty(shape, dtype=torch.uint8, device=self.device)
+
+        self.workspace = empty(megamoe_mxfp4_workspace_bytes(self.d))
+        self.w1q, self.w1s = empty(E, 2 * I, K // 2), empty(E, 2 * I, K // 32)
+        self.w2q, self.w2s = empty(E, K, I // 2), empty(E, K, I // 32)
+
+    def load_weights(self, w1, w2):
+        """w1 [E, 2I, K], w2 [E, K, I], fp32, fp16 or bf16: rows over the reduction."""
+        d = self.d
+        _shape("w1", w1, d.E, 2 * d.I, d.K)
+        _shape("w2", w2, d.E, d.K, d.I)
+        for w, q, s in ((w1, self.w1q, self.w1s), (w2, self.w2q, self.w2s)):
+            megamoe_mxfp4_quant(w.reshape(-1, w.shape[2]), q.view(-1, q.shape[2]),
+                                s.view(-1, s.shape[2]))
+
+    def route(self, logits, bias=None, renormalize=True):
+        """Router logits [M, E] -> expert_idx and probs for forward."""
+        return _route(self.d, logits, bias, renormalize)
+
+    def forward(self, x, expert_idx, probs, out=None):
+        if out is None:
+            out = torch.empty((self.d.M, self.d.K), dtype=torch.bfloat16, device=self.device)
+        megamoe_forward_mxfp4(self.d, x, expert_idx, probs, self.w1q, self.w1s, self.w2q,
+                              self.w2s, out, self.workspace)
+        return out
+
+    def last_error(self) -> int:
+        """Routes that the last forward dropped."""
         return megamoe_last_error(self.workspace)
+
+
+def _route(d, logits, bias, renormalize):
+    ids = torch.empty((d.M, d.top_k), dtype=torch.int32, device=logits.device)
+    probs = torch.empty((d.M, d.top_k), dtype=torch.float32, device=logits.device)
+    megamoe_route(d, logits, ids, probs, bias=bias, renormalize=renormalize)
+    return ids, probs

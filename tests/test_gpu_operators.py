@@ -619,3 +619,48 @@ def test_two_streams():
     torch.cuda.synchronize()
     for c in cases:
         assert same_bits(c[13], c[10][0]) and same_bits(c[14], c[10][1])
+
+
+def test_holders():
+    """The holder classes: router into the int8 layer, whole and of few tokens, and into the MXFP4 layer."""
+    M, K, E, top_k, I = 5, 512, 8, 3, 256
+    w, inp, dev, d, w1p, w2p = few_case(M, K, E, top_k, I, seed=11)
+    logits = torch.randn((M, E), generator=torch.Generator().manual_seed(4)).half().cuda()
+    logits[1] = float("nan")
+    moe = MM.MegaMoE(M, K, E, top_k, I)
+    moe.load_weights(dev["w1"], dev["scale1"], dev["w2"], dev["scale2"])
+    ids, probs = moe.route(logits)
+    whole = moe.forward(dev["x"], ids, probs)
+    assert moe.last_error() == top_k
+    few = moe.forward_few(dev["x"], ids, probs)
+    assert moe.last_error() == top_k and same_bits(whole, few) and (whole[1] == 0).all()
+    with pytest.raises(MM.MegaMoEError):
+        MM.MegaMoE(17, K, E, top_k, I).forward_few(dev["x"], ids, probs)
+
+    g = torch.Generator(device="cuda").manual_seed(12)
+    w1 = (torch.randn((E, 2 * I, K), generator=g, **CU) / K ** 0.5).bfloat16()
+    w2 = (torch.randn((E, K, I), generator=g, **CU) / I ** 0.5).bfloat16()
+    mx = MM.MegaMoEMXFP4(M, K, E, top_k, I)
+    mx.load_weights(w1, w2)
+    ids, probs = mx.route(logits, bias=torch.ones(E, **CU), renormalize=False)
+    out = mx.forward(dev["x"], ids, probs)
+    assert mx.last_error() == top_k
+    q1, s1 = run_quant(w1.view(-1, K))
+    q2, s2 = run_quant(w2.view(-1, I))
+    want, _ = mx_forward(mx.d, dev["x"], ids, probs, (q1.view(E, 2 * I, -1), s1.view(E, 2 * I, -1)),
+                         (q2.view(E, K, -1), s2.view(E, K, -1)))
+    assert same_bits(out, want) and (out[1] == 0).all()
+
+
+def test_few_refuses_wrong_sizes():
+    w, inp, dev, d, w1p, w2p = few_case(2, 256, 4, 2, 128, seed=1)
+    out = torch.empty((2, 256), dtype=torch.bfloat16, **CU)
+    ws = torch.empty(MM.megamoe_few_workspace_bytes(d), dtype=torch.uint8, **CU)
+    good = dict(x=dev["x"], expert_idx=dev["expert_idx"], probs=dev["probs"], w1p=w1p, scale1=dev["scale1"],
+                w2p=w2p, scale2=dev["scale2"], out=out, workspace=ws)
+    for name, bad in (("w1p", w1p[:-16]), ("w2p", w2p[:-16]), ("scale1", dev["scale1"][:, :-4].contiguous()),
+                      ("scale2", dev["scale2"][:-1]), ("x", dev["x"][:1]), ("out", out[:, :128].contiguous())):
+        with pytest.raises(ValueError):
+            MM.megamoe_forward_few(d, **{**good, name: bad})
+    with pytest.raises(MM.MegaMoEError):
+        MM.megamoe_forward_few(d, **{**good, "workspace": ws[:-256]})
