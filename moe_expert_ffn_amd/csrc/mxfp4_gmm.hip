@@ -205,6 +205,13 @@ __device__ __forceinline__ void mx_short_scales(const MxGmmParams &p, const MxTi
     }
 }
 
+// Weights are copied with the non-temporal hint: whoever shares a block of them asks for it at
+// the same time.  (K = 7168, I = 2048, E = 32, top_k = 8, gmm1 / gmm2 in us with it and without: 1 token
+// 22.8 / - and 25.3, 128 tokens 90 and 95, 512 tokens - / 74 and 81, after other work has filled the
+// caches 120 / 91 and 150 / 111; 2048 tokens 319 / 197 and 331 / 206.  Where one expert has a
+// dozen row blocks, which pass in two or more rounds, it costs 3%: gmm2 of 4096 skewed tokens 166 and
+// 160.)  Scales are not: a copy takes 16 bytes of a line.  (With it 128 tokens took 103.)
+//
 // The copies of stage s into slot `slot`, and of scales, with every second stage, into scale buffer
 // `sbuf`: WC + SC of weight rows and scales, ac of rows.
 template <typename G>
@@ -229,7 +236,7 @@ struct MxIssueW {
     }
     __device__ __forceinline__ void copy(int i) const {  // 0 <= i < N
         if (i < G::WC) {
-            dma16(gw, c.voff_w[i], at + i * 1024);
+            dma16_nt(gw, c.voff_w[i], at + i * 1024);
         } else if (scales) {
             const int k = mx_scale_copy<G>(i - G::WC, wave);
             const bool w = k < G::WR / 64;
