@@ -320,13 +320,12 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // are multiplied: those are in registers by then, so behind it the rows of stage s + 2 are
 // copied, and the first fragments of stage s + 1 are read.
 //
-// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 302 us, 3.2 PFLOP/s of the 6.5
-// above, gmm2 192; 512 tokens: 110 and 78.  Copies and reads without products take
-// nine tenths of that and products without copies eight, so neither hides the other
-// altogether, and with operands of zero the same work takes three quarters of the time:
-// the card lowers its clock under it.  Words of later stages fetched ahead into the
-// L2, non-temporal stores (gmm2 of 4096 tokens 176 -> 235 us) and 64-byte
-// pieces of a row to a store gave nothing or less.
+// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 285 to 313 us, 3.1 to 3.4 PFLOP/s of
+// the 6.5 above, gmm2 188; 512 tokens: 105 and 75, 128 tokens gmm1 86 (weights at 5.9
+// TB/s).  On operands of zero, for which the card keeps its clock, gmm1 of 2048
+// tokens took 254 us where random ones took 329, 209 without the copies and 264 without the products.
+// What gave nothing or less: words of later stages fetched ahead into the L2, non-temporal
+// stores (gmm2 of 4096 tokens 176 -> 235 us), 64-byte pieces of a row to a store.
 //
 // The grid is persistent.  While a tile is multiplied the workgroup looks up its
 // next one, whose first two stages are copied in this one's last two, so that
@@ -651,8 +650,8 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
 // Few rows per expert: the product streams weights.  Tiles of at most 64 rows by 128
 // weight rows; two workgroups fit a CU, so that one copies while the other looks up its tile,
 // waits for its first stage or stores.  Three slots: two stages are under way while one is
-// multiplied.  At the sizes above one token takes 21 us and 12 (weights of its eight
-// experts at 5.8 TB/s), 128 tokens 95 and 57 (5.3).
+// multiplied.  At the sizes above one token takes 22 us and 12 (weights of its eight
+// experts at 5.6 TB/s); gmm2 of 128 tokens 55.
 template <typename G, int NP>
 __device__ __forceinline__ void mx_narrow(const MxGmmParams &p, const MxTile &t, const MxCopies<G> &c,
                                           const MxLds &l) {
@@ -783,10 +782,12 @@ static void launch_variant(const MxGmmParams &p, bool narrow, int cu_count, hipS
 
 hipError_t launch_mxfp4_gmm(const MxGmmParams &p, bool swiglu, int cu_count, hipStream_t stream) {
     const int mean = (p.R + p.E - 1) / p.E;
-    // Measured on both sides, gmm1 / gmm2 at K = 7168, I = 2048, E = 32, top_k = 8, in us: 1 token
-    // narrow 24 / 12, wide 44 / 16; 32 mean rows 96 / 56 and 103 / 60; 50 rows 110 / 60 and 108 / 64;
-    // 64 rows 130 / 70 and 114 / 70.  At K = 4096, I = 1408, E = 64, 48 mean rows: 83 / 53 and 85 / 56.
-    const bool narrow = mean <= 48;
+    // Measured on both sides, narrow and wide in us, at uniform / Zipf(1.2) routing.  GMM1 at K = 7168,
+    // I = 2048, E = 32: mean 2 rows 78 / 63 and 83 / 79, 16 rows 88 / 98 and 90 / 92, 24 rows 92 / 113 and
+    // 92 / 97, 32 rows 95 / 114 and 91 / 98; at K = 4096, I = 1408, E = 64: 24 rows 76 / 89 and 81 / 97, 36
+    // rows 84 / 99 and 84 / 96.  GMM2, with half as many weight rows to a tile of output: 32 rows 60 / 68 and
+    // 59 / 67, 48 rows 63 / 73 and 61 / 79, 64 rows 83 / 81 and 65 / 95.
+    const bool narrow = mean <= (swiglu ? 28 : 48);
     if (swiglu) launch_variant<true>(p, narrow, cu_count, stream);
     else launch_variant<false>(p, narrow, cu_count, stream);
     return hipGetLastError();
