@@ -664,3 +664,59 @@ def test_few_refuses_wrong_sizes():
             MM.megamoe_forward_few(d, **{**good, name: bad})
     with pytest.raises(MM.MegaMoEError):
         MM.megamoe_forward_few(d, **{**good, "workspace": ws[:-256]})
+
+
+# ---------------------------------------------------------------------------------------------
+# offsets past 32 bits
+
+
+def test_quant_past_32_bits():
+    rows, cols = 600_000, 8192  # 4.9e9 elements, 9.8 GB
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, **CU)
+    tail = torch.randn((77, cols), generator=torch.Generator(device="cuda").manual_seed(0), **CU).bfloat16()
+    x[-77:] = tail
+    q, s = run_quant(x)
+    qt, st = run_quant(tail)
+    assert torch.equal(q[-77:], qt) and torch.equal(s[-77:], st)
+    back = torch.full_like(x, 7.0)
+    MM.megamoe_mxfp4_dequant(q, s, back)
+    assert same_bits(back[-77:], mx_values64(qt, st).bfloat16()) and bool((back[:-77].amax() == 0).item())
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_gmm_past_32_bits(rows):
+    """Weights of 8.6 and 4.3 GB, used at their far end, with narrow and wide tiles."""
+    M, K, E, top_k, I = rows * 256 // 64, 8192, 256, 64, 4096
+    if rows == 3:
+        M, top_k = 6, 1
+    counts = [0] * E
+    counts[1], counts[E - 3], counts[E - 1] = 1, rows // 2, rows
+    for first in (True, False):
+        N, red = (2 * I, K) if first else (K, I)
+        d = MM.dims(M, K, E, top_k, I)
+        route, cumsum = groups(counts, M, top_k, 5)
+        a = mx_random((M,), K, 1.0, 1) if first else mx_random((M * top_k,), I, 1.0, 1)
+        wq = torch.zeros((E, N, red // 2), dtype=torch.uint8, **CU)
+        ws = torch.full((E, N, red // 32), 127, dtype=torch.uint8, **CU)
+        for e in (1, E - 3, E - 1):
+            wq[e], ws[e] = mx_random((N,), red, 1.0 / red ** 0.5, 7 + e)
+        y = run_gmm(first, d, *a, route, cumsum, wq, ws)
+        ref, tol = gmm_reference(first, *a, route, cumsum, wq, ws, top_k)
+        n = sum(counts)
+        assert ((y[:n].double() - ref[:n]).abs() <= tol[:n]).all()
+        del wq, ws, ref, tol
+
+
+def test_few_past_32_bits():
+    M, K, E, top_k, I = 3, 8192, 256, 6, 4096
+    moe = MM.MegaMoE(M, K, E, top_k, I)  # packed weights of 17 and 8.6 GB
+    g = torch.Generator(device="cuda").manual_seed(3)
+    moe.w1p.random_(-127, 128, generator=g)
+    moe.w2p.random_(-127, 128, generator=g)
+    moe.scale1 = torch.rand((E, 2 * I), generator=g, **CU) * 1e-3
+    moe.scale2 = torch.rand((E, K), generator=g, **CU) * 1e-3
+    logits = torch.randn((M, E), generator=g, **CU)
+    logits[:, E - 2:] += 9
+    ids, probs = moe.route(logits)
+    x = torch.randn((M, K), generator=g, **CU).half()
+    assert same_bits(moe.forward_few(x, ids, probs), moe.forward(x, ids, probs))
