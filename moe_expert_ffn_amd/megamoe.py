@@ -323,18 +323,38 @@ def megamoe_last_error(workspace, stream=None) -> int:
 
 
 def _type(t: torch.Tensor) -> int:
-    if t.dtype not in _TYPES:
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
         raise TypeError(f"expected one of {sorted(map(str, _TYPES))}, got {t.dtype}")
-    return _TYPES[t.dtype]
+    return kind
 
 
-def _launch(name: str, tensors, args, stream) -> None:
-    """Calls the entry point `name` with args and the stream, on the device of the tensors: all
-    have to lie there, whichever device is current.  Without a stream, that device's current one."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on one device")
+def _device(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on the GPU")
+    return dev
+
+
+def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
+    """The address of t, which has to be contiguous and of that type and shape (None: any) on
+    device dev.  One function and plain integers: at one token the call takes longer than
+    the kernel."""
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        _device(t)
+        raise ValueError("tensors must be on one device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _launch(name: str, dev: int, stream, *args) -> None:
+    """Calls the entry point `name` with args and the stream, on the tensors' device, whichever is
+    current.  Without a stream, that device's current one."""
     if stream is None:  # the same handle as torch.cuda.current_stream(dev).cuda_stream, sooner
         handle = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device_index != dev:
@@ -342,7 +362,7 @@ def _launch(name: str, tensors, args, stream) -> None:
     else:
         handle = stream.cuda_stream
     fn = getattr(_lib or load(), name)
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -351,27 +371,20 @@ def _launch(name: str, tensors, args, stream) -> None:
         raise MegaMoEError(name, rc)
 
 
-def _shape(name: str, t: torch.Tensor, *shape: int) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-
-
 def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, stream=None):
-    _shape("logits", logits, d.M, d.E)
-    _shape("expert_idx", expert_idx, d.M, d.top_k)
-    _shape("probs", probs, d.M, d.top_k)
-    if bias is not None:
-        _shape("bias", bias, d.E)
-    args = (ctypes.byref(d), _ptr(logits), _type(logits), _ptr(bias, torch.float32),
-            int(bool(renormalize)), _ptr(expert_idx, torch.int32), _ptr(probs, torch.float32))
-    _launch("megamoe_route", (logits, bias, expert_idx, probs), args, stream)
+    M, E, k, dev = d.M, d.E, d.top_k, _device(logits)
+    _launch("megamoe_route", dev, stream, ctypes.byref(d), _at("logits", logits, None, (M, E), dev),
+            _type(logits), None if bias is None else _at("bias", bias, torch.float32, (E,), dev),
+            1 if renormalize else 0, _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
+            _at("probs", probs, torch.float32, (M, k), dev))
 
 
-def _packed(name: str, w: torch.Tensor, d, k: int, n: int) -> None:
+def _packed(name: str, w: torch.Tensor, d, k: int, n: int, dev: int) -> int:
     """Packed weights of E experts' k by n: columns in whole blocks of 256."""
     need = d.E * k * ((n + 255) // 256 * 256)
     if w.numel() < need:
         raise ValueError(f"{name}: expected at least {need} elements, got {w.numel()}")
+    return _at(name, w, torch.int8, None, dev)
 
 
 def megamoe_few_workspace_bytes(d: megamoe_dims) -> int:
@@ -383,81 +396,68 @@ def megamoe_few_workspace_bytes(d: megamoe_dims) -> int:
 
 def megamoe_forward_few(d, x, expert_idx, probs, w1p, scale1, w2p, scale2, out, workspace,
                         stream=None):
-    _shape("x", x, d.M, d.K)
-    _shape("expert_idx", expert_idx, d.M, d.top_k)
-    _shape("probs", probs, d.M, d.top_k)
-    _packed("w1p", w1p, d, d.K, 2 * d.I)
-    _shape("scale1", scale1, d.E, 2 * d.I)
-    _packed("w2p", w2p, d, d.I, d.K)
-    _shape("scale2", scale2, d.E, d.K)
-    _shape("out", out, d.M, d.K)
-    args = (ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-            _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
-            _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(out, torch.bfloat16),
-            _ptr(workspace), workspace.numel() * workspace.element_size())
-    _launch("megamoe_forward_few", (x, expert_idx, probs, w1p, scale1, w2p, scale2, out, workspace),
-            args, stream)
+    M, K, E, k, I, dev = d.M, d.K, d.E, d.top_k, d.I, _device(x)
+    _launch("megamoe_forward_few", dev, stream, ctypes.byref(d),
+            _at("x", x, torch.float16, (M, K), dev),
+            _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
+            _at("probs", probs, torch.float32, (M, k), dev),
+            _packed("w1p", w1p, d, K, 2 * I, dev),
+            _at("scale1", scale1, torch.float32, (E, 2 * I), dev),
+            _packed("w2p", w2p, d, I, K, dev),
+            _at("scale2", scale2, torch.float32, (E, K), dev),
+            _at("out", out, torch.bfloat16, (M, K), dev),
+            _at("workspace", workspace, None, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def _rows_cols(x: torch.Tensor) -> tuple[int, int]:
     if x.dim() != 2:
         raise ValueError(f"x: expected [rows, cols], got {tuple(x.shape)}")
-    return tuple(x.shape)
+    return x.shape
 
 
-def _mx_rows(q: torch.Tensor, scale: torch.Tensor, rows: int, cols: int, valid_rows) -> None:
-    _shape("q", q, rows, cols // 2)
-    _shape("scale", scale, rows, cols // 32)
-    if valid_rows is not None and valid_rows.numel() != 1:
+def _valid(valid_rows, dev: int):
+    if valid_rows is None:
+        return None
+    if valid_rows.numel() != 1:
         raise ValueError("valid_rows: expected one element")
+    return _at("valid_rows", valid_rows, torch.int32, None, dev)
 
 
 def megamoe_mxfp4_quant(x, q, scale, valid_rows=None, stream=None):
     """x [rows, cols] fp32, fp16 or bf16 -> q uint8 [rows, cols / 2], scale uint8
     [rows, cols / 32].  valid_rows: int32 device tensor of one element."""
-    rows, cols = _rows_cols(x)
-    _mx_rows(q, scale, rows, cols, valid_rows)
-    args = (_ptr(x), _type(x), rows, cols, _ptr(valid_rows, torch.int32), _ptr(q, torch.uint8),
-            _ptr(scale, torch.uint8))
-    _launch("megamoe_mxfp4_quant", (x, q, scale, valid_rows), args, stream)
+    (rows, cols), dev = _rows_cols(x), _device(x)
+    _launch("megamoe_mxfp4_quant", dev, stream, _at("x", x, None, None, dev), _type(x), rows, cols,
+            _valid(valid_rows, dev), _at("q", q, torch.uint8, (rows, cols // 2), dev),
+            _at("scale", scale, torch.uint8, (rows, cols // 32), dev))
 
 
 def megamoe_mxfp4_dequant(q, scale, x, valid_rows=None, stream=None):
-    rows, cols = _rows_cols(x)
-    _mx_rows(q, scale, rows, cols, valid_rows)
-    args = (_ptr(q, torch.uint8), _ptr(scale, torch.uint8), rows, cols,
-            _ptr(valid_rows, torch.int32), _ptr(x), _type(x))
-    _launch("megamoe_mxfp4_dequant", (q, scale, x, valid_rows), args, stream)
-
-
-def _mx_weights(name: str, d, q: torch.Tensor, s: torch.Tensor, rows: int, cols: int) -> None:
-    _shape(name + "q", q, d.E, rows, cols // 2)
-    _shape(name + "s", s, d.E, rows, cols // 32)
+    (rows, cols), dev = _rows_cols(x), _device(x)
+    _launch("megamoe_mxfp4_dequant", dev, stream, _at("q", q, torch.uint8, (rows, cols // 2), dev),
+            _at("scale", scale, torch.uint8, (rows, cols // 32), dev), rows, cols,
+            _valid(valid_rows, dev), _at("x", x, None, None, dev), _type(x))
 
 
 def megamoe_mxfp4_gmm1(d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, stream=None):
-    R = d.M * d.top_k
-    _mx_rows(xq, xs, d.M, d.K, None)
-    _shape("sorted_route", sorted_route, R)
-    _shape("expert_cumsum", expert_cumsum, d.E)
-    _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
-    _shape("y", y, R, d.I)
-    args = (ctypes.byref(d), _ptr(xq, torch.uint8), _ptr(xs, torch.uint8),
-            _ptr(sorted_route, torch.int32), _ptr(expert_cumsum, torch.int32),
-            _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8), _ptr(y, torch.bfloat16))
-    _launch("megamoe_mxfp4_gmm1", (xq, xs, sorted_route, expert_cumsum, w1q, w1s, y), args, stream)
+    M, K, E, I, dev = d.M, d.K, d.E, d.I, _device(xq)
+    R, u8, i32 = M * d.top_k, torch.uint8, torch.int32
+    _launch("megamoe_mxfp4_gmm1", dev, stream, ctypes.byref(d), _at("xq", xq, u8, (M, K // 2), dev),
+            _at("xs", xs, u8, (M, K // 32), dev), _at("sorted_route", sorted_route, i32, (R,), dev),
+            _at("expert_cumsum", expert_cumsum, i32, (E,), dev),
+            _at("w1q", w1q, u8, (E, 2 * I, K // 2), dev), _at("w1s", w1s, u8, (E, 2 * I, K // 32), dev),
+            _at("y", y, torch.bfloat16, (R, I), dev))
 
 
 def megamoe_mxfp4_gmm2(d, yq, ys, expert_cumsum, w2q, w2s, gmm2_out, stream=None):
-    R = d.M * d.top_k
-    _mx_rows(yq, ys, R, d.I, None)
-    _shape("expert_cumsum", expert_cumsum, d.E)
-    _mx_weights("w2", d, w2q, w2s, d.K, d.I)
-    _shape("gmm2_out", gmm2_out, R, d.K)
-    args = (ctypes.byref(d), _ptr(yq, torch.uint8), _ptr(ys, torch.uint8),
-            _ptr(expert_cumsum, torch.int32), _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8),
-            _ptr(gmm2_out, torch.float16))
-    _launch("megamoe_mxfp4_gmm2", (yq, ys, expert_cumsum, w2q, w2s, gmm2_out), args, stream)
+    K, E, I, dev = d.K, d.E, d.I, _device(yq)
+    R, u8 = d.M * d.top_k, torch.uint8
+    _launch("megamoe_mxfp4_gmm2", dev, stream, ctypes.byref(d), _at("yq", yq, u8, (R, I // 2), dev),
+            _at("ys", ys, u8, (R, I // 32), dev),
+            _at("expert_cumsum", expert_cumsum, torch.int32, (E,), dev),
+            _at("w2q", w2q, u8, (E, K, I // 2), dev), _at("w2s", w2s, u8, (E, K, I // 32), dev),
+            _at("gmm2_out", gmm2_out, torch.float16, (R, K), dev))
 
 
 def megamoe_mxfp4_workspace_bytes(d: megamoe_dims) -> int:
@@ -469,18 +469,16 @@ def megamoe_mxfp4_workspace_bytes(d: megamoe_dims) -> int:
 
 def megamoe_forward_mxfp4(d, x, expert_idx, probs, w1q, w1s, w2q, w2s, out, workspace,
                           stream=None):
-    _shape("x", x, d.M, d.K)
-    _shape("expert_idx", expert_idx, d.M, d.top_k)
-    _shape("probs", probs, d.M, d.top_k)
-    _mx_weights("w1", d, w1q, w1s, 2 * d.I, d.K)
-    _mx_weights("w2", d, w2q, w2s, d.K, d.I)
-    _shape("out", out, d.M, d.K)
-    args = (ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-            _ptr(probs, torch.float32), _ptr(w1q, torch.uint8), _ptr(w1s, torch.uint8),
-            _ptr(w2q, torch.uint8), _ptr(w2s, torch.uint8), _ptr(out, torch.bfloat16),
-            _ptr(workspace), workspace.numel() * workspace.element_size())
-    _launch("megamoe_forward_mxfp4", (x, expert_idx, probs, w1q, w1s, w2q, w2s, out, workspace),
-            args, stream)
+    M, K, E, k, I, dev, u8 = d.M, d.K, d.E, d.top_k, d.I, _device(x), torch.uint8
+    _launch("megamoe_forward_mxfp4", dev, stream, ctypes.byref(d),
+            _at("x", x, torch.float16, (M, K), dev),
+            _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
+            _at("probs", probs, torch.float32, (M, k), dev),
+            _at("w1q", w1q, u8, (E, 2 * I, K // 2), dev), _at("w1s", w1s, u8, (E, 2 * I, K // 32), dev),
+            _at("w2q", w2q, u8, (E, K, I // 2), dev), _at("w2s", w2s, u8, (E, K, I // 32), dev),
+            _at("out", out, torch.bfloat16, (M, K), dev),
+            _at("workspace", workspace, None, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def megamoe_set_overlap(mode: int) -> None:
@@ -561,9 +559,10 @@ class MegaMoEMXFP4:
     def load_weights(self, w1, w2):
         """w1 [E, 2I, K], w2 [E, K, I], fp32, fp16 or bf16: rows over the reduction."""
         d = self.d
-        _shape("w1", w1, d.E, 2 * d.I, d.K)
-        _shape("w2", w2, d.E, d.K, d.I)
-        for w, q, s in ((w1, self.w1q, self.w1s), (w2, self.w2q, self.w2s)):
+        for w, q, s, shape in ((w1, self.w1q, self.w1s, (d.E, 2 * d.I, d.K)),
+                               (w2, self.w2q, self.w2s, (d.E, d.K, d.I))):
+            if w.shape != shape:
+                raise ValueError(f"expected weights of shape {shape}, got {tuple(w.shape)}")
             megamoe_mxfp4_quant(w.reshape(-1, w.shape[2]), q.view(-1, q.shape[2]),
                                 s.view(-1, s.shape[2]))
 
