@@ -84,9 +84,19 @@ __global__ __launch_bounds__(kRouteBlock) void route_topk_kernel(
     const float none = -__builtin_inff();
     const bool mine_in = gl * V < E;  // with VEC all of the lane's experts exist, or none
 
-    float add[V];
+    float add[V] = {};
+    if (bias) {
+        if constexpr (VEC) {
+            typedef float word __attribute__((ext_vector_type(4)));
+            if (mine_in)
 #pragma unroll
-    for (int j = 0; j < V; ++j) add[j] = bias && gl * V + j < E ? bias[gl * V + j] : 0.0f;
+                for (int j = 0; j < V; j += 4)
+                    *reinterpret_cast<word *>(add + j) = *reinterpret_cast<const word *>(bias + gl * V + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) add[j] = gl * V + j < E ? bias[gl * V + j] : 0.0f;
+        }
+    }
 
     for (int t = blockIdx.x * kRouteTokens + tok; t < M; t += gridDim.x * kRouteTokens) {
         const T *row = logits + (size_t)t * E;
