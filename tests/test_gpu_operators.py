@@ -720,3 +720,37 @@ def test_few_past_32_bits():
     ids, probs = moe.route(logits)
     x = torch.randn((M, K), generator=g, **CU).half()
     assert same_bits(moe.forward_few(x, ids, probs), moe.forward(x, ids, probs))
+
+
+@pytest.mark.parametrize("M", [1, 3, 260])
+def test_mxfp4_layer_edge_routes(M):
+    """Every route dropped; one expert twice in a token; one expert alone; rows of a token behind it left out."""
+    K, E, I = 256, 3, 128
+    d, x, _, w1, w2 = mx_layer(M, K, E, 2, I, seed=40 + M)
+    probs = torch.full((M, 2), 0.25, **CU)
+    ids = torch.full((M, 2), -1, dtype=torch.int32, **CU)
+    ids[:, 1] = E
+    out, dropped = mx_forward(d, x, ids, probs, w1, w2)
+    assert dropped == 2 * M and (out == 0).all()
+    ids[:] = 2
+    twice, dropped = mx_forward(d, x, ids, probs, w1, w2)
+    assert dropped == 0
+    d1 = MM.dims(M, K, 1, 1, I)
+    one = torch.zeros((M, 1), dtype=torch.int32, **CU)
+    alone, dropped = mx_forward(d1, x, one, torch.full((M, 1), 0.5, **CU), [t[2:].contiguous() for t in w1],
+                                [t[2:].contiguous() for t in w2])
+    # a quarter of a value and a quarter more are half of it, exactly
+    assert dropped == 0 and same_bits(twice, alone) and torch.isfinite(alone.float()).all() and (alone != 0).any()
+    ids[::2] = -1
+    half, dropped = mx_forward(d, x, ids, probs, w1, w2)
+    assert (half[::2] == 0).all() and same_bits(half[1::2], twice[1::2])
+
+
+def test_valid_rows_from_a_view():
+    """The row count read from the last element of a cumulative sum, at an address aligned to 4 bytes."""
+    x = torch.randn((9, 64), generator=torch.Generator(device="cuda").manual_seed(0), **CU)
+    cum = torch.tensor([1, 2, 5], dtype=torch.int32, **CU)
+    q, s = torch.full((9, 32), 9, dtype=torch.uint8, **CU), torch.full((9, 2), 9, dtype=torch.uint8, **CU)
+    MM.megamoe_mxfp4_quant(x, q, s, valid_rows=cum[-1:])
+    qa, sa = run_quant(x)
+    assert torch.equal(q[:5], qa[:5]) and torch.equal(s[:5], sa[:5]) and (q[5:] == 9).all() and (s[5:] == 9).all()
