@@ -343,7 +343,8 @@ int megamoe_mxfp4_gmm2(const megamoe_dims *d, const uint8_t *yq, const uint8_t *
 
 /* The whole layer with MXFP4 experts: route sort, megamoe_mxfp4_quant of x,
  * megamoe_mxfp4_gmm1, megamoe_mxfp4_quant of y, megamoe_mxfp4_gmm2 and the combine
- * of megamoe_unpermute (with no row scale).  x, expert_idx, probs and out as in
+ * of megamoe_unpermute (with no row scale); the same bits, but y is quantised before
+ * it leaves the first product.  x, expert_idx, probs and out as in
  * megamoe_forward, dropped routes through megamoe_last_error. */
 int megamoe_mxfp4_workspace_bytes(const megamoe_dims *d, size_t *bytes);
 int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_t *expert_idx,

@@ -145,7 +145,8 @@ struct MxGmmParams {
     const uint8_t *w, *w_scale;  // [E, N or 2 N, Kred / 2], [E, N or 2 N, Kred / 32]
     const int32_t *a_route;      // nullable: A row d is row a_route[d] / a_div of a
     const int32_t *cumsum;       // [E] inclusive row prefix over experts
-    uint16_t *c;                 // [R, N]
+    uint16_t *c;                 // [R, N], or with SwiGLU, where cq is not null:
+    uint8_t *cq, *cs;            // [R, N / 2], [R, N / 32], the same rows as MXFP4
     int R, E, N, Kred, a_div;
     uint32_t a_div_inv;          // ceil(2^32 / a_div), for a_div > 1
 };

@@ -242,7 +242,7 @@ int check_few(const megamoe_dims *d) {
 
 // workspace of the MXFP4 forward
 struct Mxfp4Layout {
-    size_t err, bcnt, eri, sorted, counts, cumsum, xq, xs, y, yq, ys, g2, total;
+    size_t err, bcnt, eri, sorted, counts, cumsum, xq, xs, yq, ys, g2, total;
 };
 Mxfp4Layout mxfp4_layout(const megamoe_dims &d) {
     const size_t M = d.M, K = d.K, I = d.I, R = M * d.top_k;
@@ -256,7 +256,6 @@ Mxfp4Layout mxfp4_layout(const megamoe_dims &d) {
     L.cumsum = o; o += align_up((size_t)d.E * 4);
     L.xq = o;     o += align_up(M * (K / 2));
     L.xs = o;     o += align_up(M * (K / 32));
-    L.y = o;      o += align_up(R * I * 2);
     L.yq = o;     o += align_up(R * (I / 2));
     L.ys = o;     o += align_up(R * (I / 32));
     L.g2 = o;     o += align_up(R * K * 2);
@@ -266,8 +265,8 @@ Mxfp4Layout mxfp4_layout(const megamoe_dims &d) {
 
 int run_mxfp4_gmm(const megamoe_dims &d, const uint8_t *a, const uint8_t *as, const int32_t *route,
                   const int32_t *cumsum, const uint8_t *w, const uint8_t *ws, uint16_t *c,
-                  bool first, hipStream_t s) {
-    const MxGmmParams p{a, as, w, ws, route, cumsum, c, d.M * d.top_k, d.E,
+                  uint8_t *cq, uint8_t *cs, bool first, hipStream_t s) {
+    const MxGmmParams p{a, as, w, ws, route, cumsum, c, cq, cs, d.M * d.top_k, d.E,
                         first ? d.I : d.K, first ? d.K : d.I, d.top_k,
                         // the high product exceeds route / top_k by route * e / (top_k 2^32) with
                         // e < top_k <= 256 and route < 2^24: by less than a step of 1 / top_k
@@ -629,8 +628,8 @@ int megamoe_mxfp4_gmm1(const megamoe_dims *d, const uint8_t *xq, const uint8_t *
     const void *ptrs[] = {xq, xs, sorted_route, expert_cumsum, w1q, w1s, y};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MEGAMOE_EINVAL;
-    return run_mxfp4_gmm(*d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, true,
-                         (hipStream_t)stream);
+    return run_mxfp4_gmm(*d, xq, xs, sorted_route, expert_cumsum, w1q, w1s, y, nullptr, nullptr,
+                         true, (hipStream_t)stream);
 }
 
 int megamoe_mxfp4_gmm2(const megamoe_dims *d, const uint8_t *yq, const uint8_t *ys,
@@ -640,8 +639,8 @@ int megamoe_mxfp4_gmm2(const megamoe_dims *d, const uint8_t *yq, const uint8_t *
     const void *ptrs[] = {yq, ys, expert_cumsum, w2q, w2s, gmm2_out};
     for (const void *p : ptrs)
         if (!aligned16(p)) return MEGAMOE_EINVAL;
-    return run_mxfp4_gmm(*d, yq, ys, nullptr, expert_cumsum, w2q, w2s, gmm2_out, false,
-                         (hipStream_t)stream);
+    return run_mxfp4_gmm(*d, yq, ys, nullptr, expert_cumsum, w2q, w2s, gmm2_out, nullptr, nullptr,
+                         false, (hipStream_t)stream);
 }
 
 int megamoe_mxfp4_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
@@ -667,7 +666,7 @@ int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_
     int32_t *sorted = (int32_t *)(base + L.sorted);
     int32_t *cumsum = (int32_t *)(base + L.cumsum);
     uint8_t *xq = (uint8_t *)(base + L.xq), *xs = (uint8_t *)(base + L.xs);
-    uint16_t *y = (uint16_t *)(base + L.y), *g2 = (uint16_t *)(base + L.g2);
+    uint16_t *g2 = (uint16_t *)(base + L.g2);
     uint8_t *yq = (uint8_t *)(base + L.yq), *ys = (uint8_t *)(base + L.ys);
     const int R = d->M * d->top_k;
     MEGAMOE_TRY(hip_status(launch_route_sort(expert_idx, R, d->E, sorted, eri,
@@ -675,10 +674,8 @@ int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_
                                              (int32_t *)(base + L.err),
                                              (int32_t *)(base + L.bcnt), s)));
     MEGAMOE_TRY(hip_status(launch_mxfp4_quant(x, kFp16, d->M, d->K, nullptr, xq, xs, s)));
-    MEGAMOE_TRY(run_mxfp4_gmm(*d, xq, xs, sorted, cumsum, w1q, w1s, y, true, s));
-    MEGAMOE_TRY(hip_status(
-        launch_mxfp4_quant(y, kBf16, R, d->I, cumsum + d->E - 1, yq, ys, s)));
-    MEGAMOE_TRY(run_mxfp4_gmm(*d, yq, ys, nullptr, cumsum, w2q, w2s, g2, false, s));
+    MEGAMOE_TRY(run_mxfp4_gmm(*d, xq, xs, sorted, cumsum, w1q, w1s, nullptr, yq, ys, true, s));
+    MEGAMOE_TRY(run_mxfp4_gmm(*d, yq, ys, nullptr, cumsum, w2q, w2s, g2, nullptr, nullptr, false, s));
     return hip_status(launch_unpermute(g2, nullptr, eri, probs, d->M, d->K, d->top_k, out, s));
 }
 

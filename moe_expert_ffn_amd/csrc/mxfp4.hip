@@ -17,17 +17,13 @@
 // above infinity, which orders above every finite value.
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mxfp4_row.hpp"
 
 namespace megamoe {
 
 constexpr int kMxBlock = 256;   // threads
 constexpr int kMxChunk = 8;     // elements of a lane
 constexpr int kMxUnroll = 4;    // chunks a lane has in flight
-
-// E8M0 byte -> the fp32 power of two (byte 0 is the subnormal 2^-127; 255 NaN)
-__device__ __forceinline__ float e8m0_f32(uint32_t b) {
-    return __uint_as_float(b == 0 ? 0x400000u : b == 255 ? 0x7fc00000u : b << 23);
-}
 
 // 8 elements as fp32
 __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
@@ -105,19 +101,8 @@ __global__ __launch_bounds__(kMxBlock) void mxfp4_quant_kernel(
             const uint32_t o = (uint32_t)__shfl_xor((int)m, off, kWave);
             m = o > m ? o : m;
         }
-        // biased exponent of max|x| - 2; below 2^-125 the scale stays 2^-127
-        const uint32_t ex = m >> 23;
-        const uint32_t b = ex == 255 ? 255 : ex < 2 ? 0 : ex - 2;
-        uint32_t w = 0;
-        if (b != 255) {
-            // v_cvt_scalef32_pk_fp4_f32 divides by the scale, rounds to nearest even and saturates
-            const float s = e8m0_f32(b);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[u][0], v[u][1], s, 0);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[u][2], v[u][3], s, 1);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[u][4], v[u][5], s, 2);
-            w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[u][6], v[u][7], s, 3);
-        }
-        q[c] = w;
+        const uint32_t b = mx_scale_byte(m);
+        q[c] = mx_codes8(v[u], b);
         if ((c & 3) == 0) scale[c >> 2] = (uint8_t)b;
     }
 }

@@ -5,13 +5,14 @@
 // values that codes and block scales stand for, in fp32 on the matrix cores:
 // v_mfma_scale_f32_32x32x64_f8f6f4 takes 32 codes of a lane (one block) with
 // their scale byte.  GMM1 ends in SwiGLU: column n meets column N + n in the same
-// lane's accumulators, and silu(p[n]) * p[N + n] goes out as bf16; GMM2's p goes
-// out as fp16.
+// lane's accumulators, and silu(p[n]) * p[N + n] goes out as bf16 or, where cq is set,
+// rounded to bf16 and then to MXFP4 as mxfp4_quant_kernel does; GMM2's p goes out as fp16.
 #include <type_traits>
 
 #include "common.hpp"
 #include "dma.hpp"
 #include "kernels.hpp"
+#include "mxfp4_row.hpp"
 #include "swiglu_row.hpp"
 
 namespace megamoe {
@@ -115,6 +116,7 @@ struct MxLds {
     uint8_t *data, *scale;
     uint32_t data_at, scale_at;  // their LDS addresses
     int32_t *route;              // [AR] rows of the tile that is copied next, as sorted routes
+    uint16_t *most;              // [4][AR] a wave's largest |y| of a row (narrow tiles)
 };
 
 // row r of tile t -> row of A; rows past the group are its last one
@@ -301,6 +303,25 @@ struct MxStage {
         else codes(row + 32 * (k & 1), place[k / 2 - 1], f[k & 1][k / 2 - 1]);
     }
 };
+
+// The larger of the bf16 pairs' absolute values, half by half.
+__device__ __forceinline__ uint32_t mx_max2(uint32_t m, uint32_t v) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, v & 0x7fff7fffu);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+}
+__device__ __forceinline__ uint32_t mx_max_half(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+// ... of lanes l and l + 32, in both
+__device__ __forceinline__ uint32_t mx_max_swap(uint32_t m) {
+    const auto x = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max(x[0], x[1]);
+}
+// codes of two groups of four bf16 columns
+__device__ __forceinline__ uint32_t mx_codes(uint2 p, uint2 q, uint32_t b) {
+    const float v[8] = {bf2f_lo(p.x), bf2f_hi(p.x), bf2f_lo(p.y), bf2f_hi(p.y),
+                        bf2f_lo(q.x), bf2f_hi(q.x), bf2f_lo(q.y), bf2f_hi(q.y)};
+    return mx_codes8(v, b);
+}
 
 // silu(u) * g for a result that is rounded to bf16: the reciprocal's last ulp is not corrected
 __device__ __forceinline__ float mx_silu_times(float u, float g) {
@@ -551,20 +572,41 @@ __device__ __forceinline__ void mx_tile(const MxGmmParams &p, const MxTile &t, M
     }
     __builtin_amdgcn_sched_barrier(0);
     const int n0 = t.nblk * G::COLS + wave * (64 / F);
+    if (SWIGLU && p.cq) {
+        // Quantised here: a row's 32 columns are one block, of lanes l and l + 32.  Their groups of
+        // four columns alternate, so each takes half of both's codes and stores 8 bytes.
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int row = 32 * i + r;
-        uint16_t *crow = p.c + (size_t)(t.row0 + row) * p.N;
+        for (int i = 0; i < NP; ++i) {
+            const uint2(&o)[4] = out[i][0];
+            uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                const auto x = __builtin_amdgcn_permlane32_swap(out[i][j][k].x, out[i][j][k + 1].x, false, false);
-                const auto y = __builtin_amdgcn_permlane32_swap(out[i][j][k].y, out[i][j][k + 1].y, false, false);
-                const int col = n0 + 32 * j + 8 * (k + g);
-                if (row < t.rows && col < p.N)
-                    *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+            for (int k = 0; k < 4; ++k) m = mx_max2(mx_max2(m, o[k].x), o[k].y);
+            const uint32_t b = mx_scale_byte(mx_max_swap(mx_max_half(m)) << 16);
+            const auto w = __builtin_amdgcn_permlane32_swap(mx_codes(o[0], o[1], b),
+                                                            mx_codes(o[2], o[3], b), false, false);
+            const size_t row = t.row0 + 32 * i + r;
+            if (32 * i + r < t.rows && n0 < p.N) {
+                *reinterpret_cast<uint2 *>(p.cq + row * (p.N / 2) + n0 / 2 + 8 * g) =
+                    make_uint2((w[0] & 0xffffu) | w[1] << 16, w[0] >> 16 | (w[1] & 0xffff0000u));
+                if (g == 0) p.cs[row * (p.N / 32) + n0 / 32] = (uint8_t)b;
             }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int row = 32 * i + r;
+            uint16_t *crow = p.c + (size_t)(t.row0 + row) * p.N;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const auto x = __builtin_amdgcn_permlane32_swap(out[i][j][k].x, out[i][j][k + 1].x, false, false);
+                    const auto y = __builtin_amdgcn_permlane32_swap(out[i][j][k].y, out[i][j][k + 1].y, false, false);
+                    const int col = n0 + 32 * j + 8 * (k + g);
+                    if (row < t.rows && col < p.N)
+                        *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+                }
+        }
     }
     // all but the last two fragments have whole rows: so many stores were made at least
     stores = n0 + 64 / F <= p.N ? NP / 2 - 1 : 0;
@@ -603,7 +645,7 @@ mxfp4_gmm_tile_kernel(MxGmmParams p) {
     if (n == 0) return;
 
     const MxLds l{s_data, s_scale + 16, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
-                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route};
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route, nullptr};
     const int tid = threadIdx.x;
     const uint32_t route_at =
         __builtin_amdgcn_readfirstlane(lds_addr(s_route) + (tid >> 6) * (kWave * 4));
@@ -717,6 +759,22 @@ __device__ __forceinline__ void mx_narrow(const MxGmmParams &p, const MxTile &t,
                                             f2h(y[2]) | (uint32_t)f2h(y[3]) << 16);
         }
         const int row = 32 * i + r;
+        if (G::SWIGLU && p.cq) {  // as above, of a block that two waves share
+            const uint32_t mine =
+                mx_max_swap(mx_max_half(mx_max2(mx_max2(mx_max2(mx_max2(0, out[0].x), out[0].y), out[1].x), out[1].y)));
+            if (g == 0) l.most[wave * G::AR + row] = (uint16_t)mine;
+            __syncthreads();
+            const uint32_t b = mx_scale_byte(max(mine, (uint32_t)l.most[(wave ^ 1) * G::AR + row]) << 16);
+            const uint32_t codes = mx_codes(out[0], out[1], b);
+            const auto w = __builtin_amdgcn_permlane32_swap(codes, codes, false, false);
+            const size_t at = t.row0 + row;
+            if (row < t.rows && n0 < p.N) {
+                *reinterpret_cast<uint32_t *>(p.cq + at * (p.N / 2) + n0 / 2 + 4 * g) =
+                    g ? w[0] >> 16 | (w[1] & 0xffff0000u) : (w[0] & 0xffffu) | w[1] << 16;
+                if (g == 0 && !(wave & 1)) p.cs[at * (p.N / 32) + n0 / 32] = (uint8_t)b;
+            }
+            continue;
+        }
         uint16_t *crow = p.c + (size_t)(t.row0 + row) * p.N;
 #pragma unroll
         for (int k = 0; k < GR; k += 2) {
@@ -736,6 +794,7 @@ mxfp4_gmm_narrow_kernel(MxGmmParams p) {
     __shared__ int s_w[4];
     __shared__ MxTile s_t;
     __shared__ int32_t s_route[G::AR];
+    __shared__ uint16_t s_most[4 * G::AR];
     __shared__ __align__(16) uint8_t s_data[3 * G::STAGE];
     __shared__ __align__(16) uint8_t s_scale[16 + 2 * G::SCALE];  // a short row's word may start 4 bytes early
 
@@ -751,7 +810,7 @@ mxfp4_gmm_narrow_kernel(MxGmmParams p) {
     __syncthreads();
     const MxTile tile = mx_uniform(s_t);
     const MxLds l{s_data, s_scale + 16, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)),
-                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route};
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_scale + 16)), s_route, s_most};
     if (p.a_route && tid < G::AR) s_route[tid] = p.a_route[tile.row0 + min(tid, tile.rows - 1)];
     __syncthreads();
     const MxCopies<G> c = mx_copies<G>(p, tile, l, 1);

@@ -754,3 +754,34 @@ def test_valid_rows_from_a_view():
     MM.megamoe_mxfp4_quant(x, q, s, valid_rows=cum[-1:])
     qa, sa = run_quant(x)
     assert torch.equal(q[:5], qa[:5]) and torch.equal(s[:5], sa[:5]) and (q[5:] == 9).all() and (s[5:] == 9).all()
+
+
+@pytest.mark.parametrize("M,I", [(5, 128), (60, 384), (130, 192 * 2), (900, 128)])
+def test_mxfp4_layer_special_values(M, I):
+    """Rows that are zero, tiny, huge, infinite or NaN: the layer, which quantises between its products in
+    registers, equals its stages, which do so in memory."""
+    K, E, top_k = 512, 4, 2
+    d, x, logits, w1, w2 = mx_layer(M, K, E, top_k, I, seed=60 + M)
+    x[0] = 0
+    x[1] *= 2.0 ** -14
+    x[2] *= 30000
+    x[3, 7] = float("inf")
+    x[4, 100] = float("nan")
+    w1[1][:, ::5] -= 60      # silu columns, and gate columns, of quite different sizes
+    w1[1][:, 1::7] += 50
+    ids, probs = run_route(logits, top_k)
+    out, _ = mx_forward(d, x, ids, probs, w1, w2)
+    R = M * top_k
+    qx, pts1 = torch.empty((M, K), dtype=torch.int8, **CU), torch.empty(R, **CU)
+    eri, srt = torch.empty(R, dtype=torch.int32, **CU), torch.empty(R, dtype=torch.int32, **CU)
+    cnt, cum = torch.empty(E, dtype=torch.int32, **CU), torch.empty(E, dtype=torch.int32, **CU)
+    ws = torch.empty(MM.megamoe_permute_workspace_bytes(d), dtype=torch.uint8, **CU)
+    MM.megamoe_permute_tokens(d, x, ids, qx, pts1, eri, srt, cnt, cum, ws)
+    y = run_gmm(True, d, *run_quant(x), srt, cum, *w1)
+    yq, ys = run_quant(y)
+    assert (ys == 255).any() and (ys < 255).any() and (ys == 0).any()
+    g2 = run_gmm(False, d, yq, ys, srt, cum, *w2)
+    byhand = torch.empty((M, K), dtype=torch.bfloat16, **CU)
+    MM.megamoe_unpermute(d, g2, torch.ones(R, **CU), eri, probs, byhand)
+    assert torch.equal(torch.isnan(out), torch.isnan(byhand)) and torch.isnan(out[4]).all()
+    assert same_bits(torch.nan_to_num(out), torch.nan_to_num(byhand))
