@@ -341,8 +341,8 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // are multiplied: those are in registers by then, so behind it the rows of stage s + 2 are
 // copied, and the first fragments of stage s + 1 are read.
 //
-// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 285 to 313 us, 3.1 to 3.4 PFLOP/s of
-// the 6.5 above, gmm2 188; 512 tokens: 105 and 75, 128 tokens gmm1 86 (weights at 5.9
+// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 280 to 320 us, 3.0 to 3.4 PFLOP/s of
+// the 6.5 above, gmm2 190; 512 tokens: 105 and 75, 128 tokens gmm1 86 (weights at 5.9
 // TB/s).  On operands of zero, for which the card keeps its clock, gmm1 of 2048
 // tokens took 254 us where random ones took 329, 209 without the copies and 264 without the products.
 // What gave nothing or less: words of later stages fetched ahead into the L2, non-temporal
