@@ -488,7 +488,8 @@ def megamoe_set_overlap(mode: int) -> None:
 
 
 class MegaMoE:
-    """Convenience holder: packed weights + workspace for one set of dims."""
+    """Convenience holder: packed weights + workspace for one set of dims.  forward and
+    forward_few share the workspace: calls of one holder belong in one order."""
 
     def __init__(self, M: int, K: int, E: int, top_k: int, I: int, device="cuda"):
         self.d = dims(M, K, E, top_k, I)
@@ -496,11 +497,9 @@ class MegaMoE:
         self.device = torch.device(device)
         self.workspace = torch.empty(megamoe_workspace_bytes(self.d), dtype=torch.uint8,
                                      device=self.device)
-        self.few_workspace = None  # where the dims allow forward_few
-        if M <= 16 and M * top_k <= 512:
-            self.few_workspace = torch.empty(megamoe_few_workspace_bytes(self.d),
-                                             dtype=torch.uint8, device=self.device)
-        self._last = self.workspace
+        # forward_few, where the dims allow it, works in the same memory (it needs less), so that
+        # the dropped-route word is that of the newest forward on the GPU, replayed graphs included
+        self.few_workspace = self.workspace if M <= 16 and M * top_k <= 512 else None
         n1, n2 = megamoe_packed_weight_bytes(self.d)
         self.w1p = torch.empty(n1, dtype=torch.int8, device=self.device)
         self.w2p = torch.empty(n2, dtype=torch.int8, device=self.device)
@@ -522,7 +521,6 @@ class MegaMoE:
             out = torch.empty((self.d.M, self.d.K), dtype=torch.bfloat16, device=self.device)
         megamoe_forward(self.d, x, expert_idx, probs, self.w1p, self.scale1, self.w2p,
                         self.scale2, out, self.workspace)
-        self._last = self.workspace
         return out
 
     def forward_few(self, x, expert_idx, probs, out=None):
@@ -533,12 +531,11 @@ class MegaMoE:
             out = torch.empty((self.d.M, self.d.K), dtype=torch.bfloat16, device=self.device)
         megamoe_forward_few(self.d, x, expert_idx, probs, self.w1p, self.scale1, self.w2p,
                             self.scale2, out, self.few_workspace)
-        self._last = self.few_workspace
         return out
 
     def last_error(self) -> int:
         """Routes that the last forward dropped."""
-        return megamoe_last_error(self._last)
+        return megamoe_last_error(self.workspace)
 
 
 class MegaMoEMXFP4:
