@@ -138,21 +138,48 @@ def _check(fn: str, rc: int) -> None:
         raise MegaMoEError(fn, rc)
 
 
-def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None):
+def _device(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on the GPU")
+    return dev
+
+
+def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None, dev: int) -> int | None:
+    """The address of t, which has to be contiguous, of that type and on device dev."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("tensors must live on the GPU")
+    if t.get_device() != dev:
+        _device(t)
+        raise ValueError("tensors must be on one device")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"expected {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _handle(dev: int, stream) -> int:
+    """The stream's handle; without one, that of the current stream of the tensors' device."""
+    if stream is None:  # the same handle as torch.cuda.current_stream(dev).cuda_stream, sooner
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream must be on the tensors' device")
+    return stream.cuda_stream
+
+
+def _launch(name: str, dev: int, stream, *args) -> None:
+    """Calls the entry point `name` with args and the stream, on the tensors' device, whichever is
+    current.  Without a stream, that device's current one."""
+    handle = _handle(dev, stream)
+    fn = getattr(_lib or load(), name)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc != MEGAMOE_OK:
+        raise MegaMoEError(name, rc)
 
 
 def megamoe_check_dims(d: megamoe_dims) -> int:
@@ -180,80 +207,90 @@ def megamoe_packed_weight_bytes(d: megamoe_dims) -> tuple[int, int]:
 
 
 def megamoe_prepack_w1(d, w1, w1p, stream=None):
-    _check("megamoe_prepack_w1", load().megamoe_prepack_w1(
-        ctypes.byref(d), _ptr(w1, torch.int8), _ptr(w1p, torch.int8), _stream(stream)))
+    dev = _device(w1)
+    _launch("megamoe_prepack_w1", dev, stream, ctypes.byref(d), _ptr(w1, torch.int8, dev),
+            _ptr(w1p, torch.int8, dev))
 
 
 def megamoe_prepack_w2(d, w2, w2p, stream=None):
-    _check("megamoe_prepack_w2", load().megamoe_prepack_w2(
-        ctypes.byref(d), _ptr(w2, torch.int8), _ptr(w2p, torch.int8), _stream(stream)))
+    dev = _device(w2)
+    _launch("megamoe_prepack_w2", dev, stream, ctypes.byref(d), _ptr(w2, torch.int8, dev),
+            _ptr(w2p, torch.int8, dev))
 
 
 def megamoe_forward(d, x, expert_idx, probs, w1p, scale1, w2p, scale2, out, workspace,
                     stream=None):
-    _check("megamoe_forward", load().megamoe_forward(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(probs, torch.float32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
-        _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(out, torch.bfloat16),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device(x)
+    _launch("megamoe_forward", dev, stream, ctypes.byref(d), _ptr(x, torch.float16, dev),
+            _ptr(expert_idx, torch.int32, dev), _ptr(probs, torch.float32, dev),
+            _ptr(w1p, torch.int8, dev), _ptr(scale1, torch.float32, dev),
+            _ptr(w2p, torch.int8, dev), _ptr(scale2, torch.float32, dev),
+            _ptr(out, torch.bfloat16, dev), _ptr(workspace, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def megamoe_permute(d, x, expert_idx, gmA, pts1, expanded_row_idx, sorted_route,
                     tokens_per_expert, expert_cumsum, workspace, stream=None):
-    _check("megamoe_permute", load().megamoe_permute(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(gmA, torch.int8), _ptr(pts1, torch.float32), _ptr(expanded_row_idx, torch.int32),
-        _ptr(sorted_route, torch.int32), _ptr(tokens_per_expert, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device(x)
+    _launch("megamoe_permute", dev, stream, ctypes.byref(d), _ptr(x, torch.float16, dev),
+            _ptr(expert_idx, torch.int32, dev), _ptr(gmA, torch.int8, dev),
+            _ptr(pts1, torch.float32, dev), _ptr(expanded_row_idx, torch.int32, dev),
+            _ptr(sorted_route, torch.int32, dev), _ptr(tokens_per_expert, torch.int32, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(workspace, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def megamoe_permute_tokens(d, x, expert_idx, qx, pts1, expanded_row_idx, sorted_route,
                            tokens_per_expert, expert_cumsum, workspace, stream=None):
-    _check("megamoe_permute_tokens", load().megamoe_permute_tokens(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(qx, torch.int8), _ptr(pts1, torch.float32), _ptr(expanded_row_idx, torch.int32),
-        _ptr(sorted_route, torch.int32), _ptr(tokens_per_expert, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device(x)
+    _launch("megamoe_permute_tokens", dev, stream, ctypes.byref(d), _ptr(x, torch.float16, dev),
+            _ptr(expert_idx, torch.int32, dev), _ptr(qx, torch.int8, dev),
+            _ptr(pts1, torch.float32, dev), _ptr(expanded_row_idx, torch.int32, dev),
+            _ptr(sorted_route, torch.int32, dev), _ptr(tokens_per_expert, torch.int32, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(workspace, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def megamoe_permute_noalloc(d, x, expert_idx, gmA, pts1, expanded_row_idx, sorted_route,
                             tokens_per_expert, expert_cumsum, dropped, stream=None):
-    _check("megamoe_permute_noalloc", load().megamoe_permute_noalloc(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(gmA, torch.int8), _ptr(pts1, torch.float32), _ptr(expanded_row_idx, torch.int32),
-        _ptr(sorted_route, torch.int32), _ptr(tokens_per_expert, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(dropped, torch.int32), _stream(stream)))
+    dev = _device(x)
+    _launch("megamoe_permute_noalloc", dev, stream, ctypes.byref(d), _ptr(x, torch.float16, dev),
+            _ptr(expert_idx, torch.int32, dev), _ptr(gmA, torch.int8, dev),
+            _ptr(pts1, torch.float32, dev), _ptr(expanded_row_idx, torch.int32, dev),
+            _ptr(sorted_route, torch.int32, dev), _ptr(tokens_per_expert, torch.int32, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(dropped, torch.int32, dev))
 
 
 def megamoe_gmm1_gather(d, qx, sorted_route, expert_cumsum, w1p, scale1, gmC, acc_dbg=None,
                         stream=None):
-    _check("megamoe_gmm1_gather", load().megamoe_gmm1_gather(
-        ctypes.byref(d), _ptr(qx, torch.int8), _ptr(sorted_route, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
-        _ptr(gmC, torch.float16), _ptr(acc_dbg, torch.int32), _stream(stream)))
+    dev = _device(qx)
+    _launch("megamoe_gmm1_gather", dev, stream, ctypes.byref(d), _ptr(qx, torch.int8, dev),
+            _ptr(sorted_route, torch.int32, dev), _ptr(expert_cumsum, torch.int32, dev),
+            _ptr(w1p, torch.int8, dev), _ptr(scale1, torch.float32, dev),
+            _ptr(gmC, torch.float16, dev), _ptr(acc_dbg, torch.int32, dev))
 
 
 def megamoe_gmm1(d, gmA, expert_cumsum, w1p, scale1, gmC, acc_dbg=None, stream=None):
-    _check("megamoe_gmm1", load().megamoe_gmm1(
-        ctypes.byref(d), _ptr(gmA, torch.int8), _ptr(expert_cumsum, torch.int32),
-        _ptr(w1p, torch.int8), _ptr(scale1, torch.float32), _ptr(gmC, torch.float16),
-        _ptr(acc_dbg, torch.int32), _stream(stream)))
+    dev = _device(gmA)
+    _launch("megamoe_gmm1", dev, stream, ctypes.byref(d), _ptr(gmA, torch.int8, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(w1p, torch.int8, dev),
+            _ptr(scale1, torch.float32, dev), _ptr(gmC, torch.float16, dev),
+            _ptr(acc_dbg, torch.int32, dev))
 
 
 def megamoe_swiglu_quant(d, gmC, pts1, expert_cumsum, q2, pts2, stream=None):
-    _check("megamoe_swiglu_quant", load().megamoe_swiglu_quant(
-        ctypes.byref(d), _ptr(gmC, torch.float16), _ptr(pts1, torch.float32),
-        _ptr(expert_cumsum, torch.int32), _ptr(q2, torch.int8), _ptr(pts2, torch.float32),
-        _stream(stream)))
+    dev = _device(gmC)
+    _launch("megamoe_swiglu_quant", dev, stream, ctypes.byref(d), _ptr(gmC, torch.float16, dev),
+            _ptr(pts1, torch.float32, dev), _ptr(expert_cumsum, torch.int32, dev),
+            _ptr(q2, torch.int8, dev), _ptr(pts2, torch.float32, dev))
 
 
 def megamoe_gmm2(d, q2, expert_cumsum, w2p, scale2, gmm2_out, acc_dbg=None, stream=None):
-    _check("megamoe_gmm2", load().megamoe_gmm2(
-        ctypes.byref(d), _ptr(q2, torch.int8), _ptr(expert_cumsum, torch.int32),
-        _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(gmm2_out, torch.float16),
-        _ptr(acc_dbg, torch.int32), _stream(stream)))
+    dev = _device(q2)
+    _launch("megamoe_gmm2", dev, stream, ctypes.byref(d), _ptr(q2, torch.int8, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(w2p, torch.int8, dev),
+            _ptr(scale2, torch.float32, dev), _ptr(gmm2_out, torch.float16, dev),
+            _ptr(acc_dbg, torch.int32, dev))
 
 
 def megamoe_gmm1_split_workspace_bytes(d: megamoe_dims) -> int:
@@ -265,11 +302,11 @@ def megamoe_gmm1_split_workspace_bytes(d: megamoe_dims) -> int:
 
 def megamoe_gmm1_gather_split(d, qx, sorted_route, expert_cumsum, w1p, scale1, gmC, split_ws,
                               stream=None):
-    _check("megamoe_gmm1_gather_split", load().megamoe_gmm1_gather_split(
-        ctypes.byref(d), _ptr(qx, torch.int8), _ptr(sorted_route, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(w1p, torch.int8), _ptr(scale1, torch.float32),
-        _ptr(gmC, torch.float16), _ptr(split_ws, torch.uint8), split_ws.numel(),
-        _stream(stream)))
+    dev = _device(qx)
+    _launch("megamoe_gmm1_gather_split", dev, stream, ctypes.byref(d), _ptr(qx, torch.int8, dev),
+            _ptr(sorted_route, torch.int32, dev), _ptr(expert_cumsum, torch.int32, dev),
+            _ptr(w1p, torch.int8, dev), _ptr(scale1, torch.float32, dev),
+            _ptr(gmC, torch.float16, dev), _ptr(split_ws, torch.uint8, dev), split_ws.numel())
 
 
 def megamoe_paired_q2_bytes(d: megamoe_dims) -> int:
@@ -282,41 +319,46 @@ def megamoe_paired_q2_bytes(d: megamoe_dims) -> int:
 def megamoe_permute_tokens_paired(d, x, expert_idx, qx, pts1, expanded_row_idx, sorted_route,
                                   tokens_per_expert, expert_cumsum, prow, workspace,
                                   stream=None):
-    _check("megamoe_permute_tokens_paired", load().megamoe_permute_tokens_paired(
-        ctypes.byref(d), _ptr(x, torch.float16), _ptr(expert_idx, torch.int32),
-        _ptr(qx, torch.int8), _ptr(pts1, torch.float32), _ptr(expanded_row_idx, torch.int32),
-        _ptr(sorted_route, torch.int32), _ptr(tokens_per_expert, torch.int32),
-        _ptr(expert_cumsum, torch.int32), _ptr(prow, torch.int32), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device(x)
+    _launch("megamoe_permute_tokens_paired", dev, stream, ctypes.byref(d),
+            _ptr(x, torch.float16, dev), _ptr(expert_idx, torch.int32, dev),
+            _ptr(qx, torch.int8, dev), _ptr(pts1, torch.float32, dev),
+            _ptr(expanded_row_idx, torch.int32, dev), _ptr(sorted_route, torch.int32, dev),
+            _ptr(tokens_per_expert, torch.int32, dev), _ptr(expert_cumsum, torch.int32, dev),
+            _ptr(prow, torch.int32, dev), _ptr(workspace, None, dev),
+            workspace.numel() * workspace.element_size())
 
 
 def megamoe_swiglu_quant_paired(d, gmC, pts1, expert_cumsum, prow, q2p, pts2, stream=None):
-    _check("megamoe_swiglu_quant_paired", load().megamoe_swiglu_quant_paired(
-        ctypes.byref(d), _ptr(gmC, torch.float16), _ptr(pts1, torch.float32),
-        _ptr(expert_cumsum, torch.int32), _ptr(prow, torch.int32), _ptr(q2p, torch.int8),
-        _ptr(pts2, torch.float32), _stream(stream)))
+    dev = _device(gmC)
+    _launch("megamoe_swiglu_quant_paired", dev, stream, ctypes.byref(d),
+            _ptr(gmC, torch.float16, dev), _ptr(pts1, torch.float32, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(prow, torch.int32, dev),
+            _ptr(q2p, torch.int8, dev), _ptr(pts2, torch.float32, dev))
 
 
 def megamoe_gmm2_paired(d, q2p, expert_cumsum, w2p, scale2, gmm2_out, acc_dbg=None,
                         stream=None):
-    _check("megamoe_gmm2_paired", load().megamoe_gmm2_paired(
-        ctypes.byref(d), _ptr(q2p, torch.int8), _ptr(expert_cumsum, torch.int32),
-        _ptr(w2p, torch.int8), _ptr(scale2, torch.float32), _ptr(gmm2_out, torch.float16),
-        _ptr(acc_dbg, torch.int32), _stream(stream)))
+    dev = _device(q2p)
+    _launch("megamoe_gmm2_paired", dev, stream, ctypes.byref(d), _ptr(q2p, torch.int8, dev),
+            _ptr(expert_cumsum, torch.int32, dev), _ptr(w2p, torch.int8, dev),
+            _ptr(scale2, torch.float32, dev), _ptr(gmm2_out, torch.float16, dev),
+            _ptr(acc_dbg, torch.int32, dev))
 
 
 def megamoe_unpermute(d, gmm2_out, pts2, expanded_row_idx, probs, out, stream=None):
-    _check("megamoe_unpermute", load().megamoe_unpermute(
-        ctypes.byref(d), _ptr(gmm2_out, torch.float16), _ptr(pts2, torch.float32),
-        _ptr(expanded_row_idx, torch.int32), _ptr(probs, torch.float32),
-        _ptr(out, torch.bfloat16), _stream(stream)))
+    dev = _device(gmm2_out)
+    _launch("megamoe_unpermute", dev, stream, ctypes.byref(d), _ptr(gmm2_out, torch.float16, dev),
+            _ptr(pts2, torch.float32, dev), _ptr(expanded_row_idx, torch.int32, dev),
+            _ptr(probs, torch.float32, dev), _ptr(out, torch.bfloat16, dev))
 
 
 def megamoe_last_error(workspace, stream=None) -> int:
     """The number of routes the last permute / forward on this workspace
     dropped (the library returns MEGAMOE_EDEVICE when it is not zero)."""
-    v = ctypes.c_int32(0)
-    rc = load().megamoe_last_error(_ptr(workspace), _stream(stream), ctypes.byref(v))
+    v, dev = ctypes.c_int32(0), _device(workspace)
+    with torch.cuda.device(dev):
+        rc = load().megamoe_last_error(_ptr(workspace, None, dev), _handle(dev, stream), ctypes.byref(v))
     if rc != MEGAMOE_EDEVICE:
         _check("megamoe_last_error", rc)
     return v.value
@@ -327,13 +369,6 @@ def _type(t: torch.Tensor) -> int:
     if kind is None:
         raise TypeError(f"expected one of {sorted(map(str, _TYPES))}, got {t.dtype}")
     return kind
-
-
-def _device(t: torch.Tensor) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must live on the GPU")
-    return dev
 
 
 def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
@@ -350,25 +385,6 @@ def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensors must be contiguous")
     return t.data_ptr()
-
-
-def _launch(name: str, dev: int, stream, *args) -> None:
-    """Calls the entry point `name` with args and the stream, on the tensors' device, whichever is
-    current.  Without a stream, that device's current one."""
-    if stream is None:  # the same handle as torch.cuda.current_stream(dev).cuda_stream, sooner
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device_index != dev:
-        raise ValueError("the stream must be on the tensors' device")
-    else:
-        handle = stream.cuda_stream
-    fn = getattr(_lib or load(), name)
-    if dev == torch._C._cuda_getDevice():
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, handle)
-    if rc != MEGAMOE_OK:
-        raise MegaMoEError(name, rc)
 
 
 def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, stream=None):
