@@ -138,7 +138,9 @@ def _check(fn: str, rc: int) -> None:
         raise MegaMoEError(fn, rc)
 
 
-def _device(t: torch.Tensor) -> int:
+def _device(t: torch.Tensor | None) -> int:
+    if t is None:  # a null pointer, which the library refuses
+        return torch._C._cuda_getDevice()
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must live on the GPU")
@@ -371,10 +373,12 @@ def _type(t: torch.Tensor) -> int:
     return kind
 
 
-def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
+def _at(name: str, t: torch.Tensor | None, dtype, shape, dev: int) -> int | None:
     """The address of t, which has to be contiguous and of that type and shape (None: any) on
     device dev.  One function and plain integers: at one token the call takes longer than
     the kernel."""
+    if t is None:
+        return None
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
@@ -390,15 +394,15 @@ def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
 def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, stream=None):
     M, E, k, dev = d.M, d.E, d.top_k, _device(logits)
     _launch("megamoe_route", dev, stream, ctypes.byref(d), _at("logits", logits, None, (M, E), dev),
-            _type(logits), None if bias is None else _at("bias", bias, torch.float32, (E,), dev),
+            0 if logits is None else _type(logits), _at("bias", bias, torch.float32, (E,), dev),
             1 if renormalize else 0, _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
             _at("probs", probs, torch.float32, (M, k), dev))
 
 
-def _packed(name: str, w: torch.Tensor, d, k: int, n: int, dev: int) -> int:
+def _packed(name: str, w: torch.Tensor | None, d, k: int, n: int, dev: int) -> int | None:
     """Packed weights of E experts' k by n: columns in whole blocks of 256."""
     need = d.E * k * ((n + 255) // 256 * 256)
-    if w.numel() < need:
+    if w is not None and w.numel() < need:
         raise ValueError(f"{name}: expected at least {need} elements, got {w.numel()}")
     return _at(name, w, torch.int8, None, dev)
 
@@ -568,15 +572,21 @@ class MegaMoEMXFP4:
         self.workspace = empty(megamoe_mxfp4_workspace_bytes(self.d))
         self.w1q, self.w1s = empty(E, 2 * I, K // 2), empty(E, 2 * I, K // 32)
         self.w2q, self.w2s = empty(E, K, I // 2), empty(E, K, I // 32)
+        for s in (self.w1s, self.w2s):
+            s.fill_(255)  # NaN: what a forward answers before load_weights
 
     def load_weights(self, w1, w2):
         """w1 [E, 2I, K], w2 [E, K, I], fp32, fp16 or bf16: rows over the reduction."""
         d = self.d
-        for w, q, s, shape in ((w1, self.w1q, self.w1s, (d.E, 2 * d.I, d.K)),
-                               (w2, self.w2q, self.w2s, (d.E, d.K, d.I))):
+        weights = ((w1, self.w1q, self.w1s, (d.E, 2 * d.I, d.K)), (w2, self.w2q, self.w2s, (d.E, d.K, d.I)))
+        for w, q, _, shape in weights:  # all of it before the first is written
             if w.shape != shape:
                 raise ValueError(f"expected weights of shape {shape}, got {tuple(w.shape)}")
-            megamoe_mxfp4_quant(w.reshape(-1, w.shape[2]), q.view(-1, q.shape[2]),
+            if _device(w) != q.get_device():
+                raise ValueError("weights must be on the holder's device")
+            _type(w)
+        for w, q, s, _ in weights:
+            megamoe_mxfp4_quant(w.reshape(-1, w.shape[2]).contiguous(), q.view(-1, q.shape[2]),
                                 s.view(-1, s.shape[2]))
 
     def route(self, logits, bias=None, renormalize=True):

@@ -139,3 +139,25 @@ def test_tensors_of_two_devices_are_refused(machine, name):
         with pytest.raises(ValueError, match="one device"):
             getattr(MM, name)(*arguments(name, kinds))
     assert machine.calls == []
+
+
+SIZED_BY = {("megamoe_mxfp4_quant", 0), ("megamoe_mxfp4_dequant", 2)}  # no sizes without these
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_nothing_for_a_tensor(name):
+    """None is a null pointer, which the library refuses with its own error."""
+    n = len(CALLS[name][1])
+    if torch.cuda.device_count():
+        pytest.skip("passes host addresses; host-only")
+    for at in range(n):
+        if CALLS[name][1][at] is WS or (name, at) in SIZED_BY:
+            continue
+        with pytest.MonkeyPatch.context() as patch:
+            patch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+            patch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+            args = arguments(name, [_Gpu0] * n)
+            args[at + CALLS[name][0]] = None
+            with pytest.raises(MM.MegaMoEError) as err:
+                getattr(MM, name)(*args)
+            assert err.value.status == 1, at

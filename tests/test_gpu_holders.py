@@ -58,3 +58,36 @@ def test_last_error_is_of_the_forward_that_ran():
         assert moe.last_error() == 1 and same_bits(out, want_one)
         assert same_bits(moe.forward_few(dev["x"], three, dev["probs"]), want_three)
         assert moe.last_error() == 3
+
+
+def test_forward_before_the_weights():
+    """Without weights the int8 forms are refused with the library's error and the MXFP4 layer
+    answers NaN; weights that are refused leave the ones before them whole."""
+    M, K, E, top_k, I = 4, 256, 8, 2, 128
+    x = torch.ones((M, K), dtype=torch.float16, **CU)
+    ids = torch.arange(M * top_k, dtype=torch.int32, **CU).view(M, top_k)
+    probs = torch.full((M, top_k), 0.5, **CU)
+    moe = MM.MegaMoE(M, K, E, top_k, I)
+    for form in (moe.forward, moe.forward_few):
+        with pytest.raises(MM.MegaMoEError) as err:
+            form(x, ids, probs)
+        assert err.value.status == 1
+
+    # the allocator hands out memory that held finite values before
+    for shape in ((E, 2 * I, K // 2), (E, 2 * I, K // 32), (E, K, I // 2), (E, K, I // 32)):
+        torch.full(shape, 120, dtype=torch.uint8, **CU)
+    mx = MM.MegaMoEMXFP4(M, K, E, top_k, I)
+    assert torch.isnan(mx.forward(x, ids, probs)).all()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w1, w2 = torch.randn((E, 2 * I, K), generator=g, **CU) / 16, torch.randn((E, K, I), generator=g, **CU) / 11
+    mx.load_weights(w1, w2)
+    want = mx.forward(x, ids, probs)
+    assert torch.isfinite(want).all() and (want != 0).any()
+    for bad, error in ((w2[:, :-1], ValueError), (w2.cpu(), ValueError), (w2.double(), TypeError)):
+        with pytest.raises(error):
+            mx.load_weights(w1 * 2, bad)
+        assert same_bits(mx.forward(x, ids, probs), want)
+    wide = torch.zeros((E, K, 2 * I), **CU)
+    wide[..., ::2] = w2
+    mx.load_weights(w1, wide[..., ::2])    # of any strides
+    assert same_bits(mx.forward(x, ids, probs), want)
