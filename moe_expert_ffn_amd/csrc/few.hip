@@ -122,7 +122,7 @@ __device__ __forceinline__ v4i few_mfma(v4i w, v4i a, v4i acc) {
 }
 
 // ---------------------------------------------------------------------------
-// K = 7168, I = 2048, E = 32, top_k = 8: 38 us at one token and 152 at 16, of 35 and 140 for
+// K = 7168, I = 2048, E = 32, top_k = 8: 38 us at one token and 152 to 160 at 16, of 35 and 140 for
 // the weights alone at 6.7 TB/s.  (With 1 group of columns 40 and 186, with 4 57 and 247.)
 constexpr int kFew1Groups = 2;  // groups of 16 columns that share the quantised rows
 
@@ -283,7 +283,7 @@ few_gmm1_kernel(FewParams p, int row_cap) {
 // whose rows fit an LDS buffer (and a chunk of I where I is long).  Twelve of its
 // waves quantise the rows of the next step while four multiply the current one,
 // so weights keep coming while y is read and rounded.  (K = 7168, I = 2048, E = 32,
-// top_k = 8: 92 us at 16 tokens and 23.5 at one, of 71 and 18 for the weights
+// top_k = 8: 94 us at 16 tokens and 23.5 at one, of 71 and 18 for the weights
 // alone; eight and eight waves took 100 and 23.4, all waves doing both in turn
 // 125 and 26.6.)
 constexpr int kFew2Threads = 1024;

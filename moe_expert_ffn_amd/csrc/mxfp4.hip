@@ -11,8 +11,8 @@
 // Both kernels are bound by HBM.  A lane owns 8 consecutive elements (one 16-byte
 // load of a 16-bit type, one 4-byte store of codes), so a wave's accesses are
 // contiguous, and a block is four lanes, whose maximum takes two lane exchanges.
-// 128 rows of 7168 fp16 take 3.6 us and 4.0 back, 16211 of 2048 bf16 17.3 us and 14.9
-// (5.3 TB/s together, what a large copy reaches).
+// 128 rows of 7168 fp16 take 3.6 us and 3.9 back, 16211 of 2048 bf16 16.5 us and 13.9
+// (84 MB each, 5.1 and 6.0 TB/s: a large copy reaches 5.2, and the codes are read back from a cache).
 // The largest |x| is an integer maximum of the bits without the sign: NaN orders
 // above infinity, which orders above every finite value.
 #include "common.hpp"

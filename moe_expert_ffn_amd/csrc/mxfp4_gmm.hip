@@ -341,10 +341,12 @@ __device__ __forceinline__ float mx_silu_times(float u, float g) {
 // are multiplied: those are in registers by then, so behind it the rows of stage s + 2 are
 // copied, and the first fragments of stage s + 1 are read.
 //
-// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 280 to 320 us, 3.0 to 3.4 PFLOP/s of
-// the 6.5 above, gmm2 190; 512 tokens: 105 and 75, 128 tokens gmm1 86 (weights at 5.9
-// TB/s).  On operands of zero, for which the card keeps its clock, gmm1 of 2048
-// tokens took 254 us where random ones took 329, 209 without the copies and 264 without the products.
+// K = 7168, I = 2048, E = 32, top_k = 8, 2048 tokens: gmm1 280 to 320 us between other kernels, 3.0 to
+// 3.4 PFLOP/s of the 6.5 above, gmm2 190 to 200; 512 tokens: 107 and 75, 128 tokens gmm1 86 (weights at 5.9
+// TB/s).  gmm1 of 2048 tokens alone, call after call, goes from 278 us to 390 as the clock comes down (to 1.8 GHz
+// in the mean of twenty calls; 2.0 between other kernels, 2.45 in gmm1 of 128 tokens).  Its matrix cores are busy in 41 to 45%
+// of the cycles, LDS in 27 to 30%, a third of those for bank conflicts.  On operands of zero, for which the card keeps its clock,
+// it took 254 us where random ones took 329, 209 without the copies and 264 without the products.
 // What gave nothing or less: words of later stages fetched ahead into the L2, non-temporal
 // stores (gmm2 of 4096 tokens 176 -> 235 us), 64-byte pieces of a row to a store.
 //

@@ -15,8 +15,8 @@
 // lanes, over the group; the first lane that holds it clears its first copy.  Only
 // the indices go through LDS.  Instruction issue bounds the kernel: 64 lanes to a
 // token would take half as long again in lane exchanges, one lane to many experts
-// more in clearing.  32768 tokens of 256 bf16 logits, top_k = 8: 13.7 us, with a
-// bias and all experts' weights 16.4 (64 lanes to a token: 53); one token 3.0.  The next
+// more in clearing.  32768 tokens of 256 bf16 logits, top_k = 8: 14 us, with a
+// bias and all experts' weights 16 (64 lanes to a token: 53); one token 3.0.  The next
 // token's logits asked for early, or more waves with fewer registers, gave nothing.
 #include "common.hpp"
 #include "kernels.hpp"
