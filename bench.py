@@ -34,6 +34,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import sys
 import time
 
@@ -97,14 +98,23 @@ def algorithmic(w, counts: np.ndarray) -> dict:
 
 
 def source_hash(path: str) -> str:
-    """Hash of a kernel source and of the headers beside it (every kernel
-    includes some of them), so that a change to either invalidates a
-    profile taken from the older code."""
+    """Hash of a kernel source and of the headers beside it that it includes,
+    directly or through another, so that a change to any of them invalidates a
+    profile taken from the older code, and one to a header of other kernels
+    does not."""
     h = hashlib.sha256()
-    d = os.path.dirname(path)
-    for p in [path] + sorted(os.path.join(d, f) for f in os.listdir(d) if f.endswith(".hpp")):
+    todo, seen = [os.path.realpath(path)], set()
+    while todo:
+        p = todo.pop()
+        if p in seen:
+            continue
+        seen.add(p)
         with open(p, "rb") as f:
-            h.update(f.read())
+            text = f.read()
+        h.update(os.path.basename(p).encode() + b"\0" + text)
+        names = re.findall(rb'^\s*#\s*include\s+"([^"]+)"', text, re.M)
+        near = (os.path.realpath(os.path.join(os.path.dirname(p), n.decode())) for n in names)
+        todo += sorted((q for q in near if os.path.exists(q)), reverse=True)
     return h.hexdigest()[:16]
 
 
