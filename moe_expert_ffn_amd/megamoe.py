@@ -173,7 +173,7 @@ def _handle(dev: int, stream) -> int:
 def _launch(name: str, dev: int, stream, *args) -> None:
     """Calls the entry point `name` with args and the stream, on the tensors' device, whichever is
     current.  Without a stream, that device's current one."""
-    handle = _handle(dev, stream)
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _handle(dev, stream)
     fn = getattr(_lib or load(), name)
     if dev == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
@@ -394,7 +394,8 @@ def _at(name: str, t: torch.Tensor | None, dtype, shape, dev: int) -> int | None
 def megamoe_route(d, logits, expert_idx, probs, bias=None, renormalize=True, stream=None):
     M, E, k, dev = d.M, d.E, d.top_k, _device(logits)
     _launch("megamoe_route", dev, stream, ctypes.byref(d), _at("logits", logits, None, (M, E), dev),
-            0 if logits is None else _type(logits), _at("bias", bias, torch.float32, (E,), dev),
+            0 if logits is None else _type(logits),
+            None if bias is None else _at("bias", bias, torch.float32, (E,), dev),
             1 if renormalize else 0, _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
             _at("probs", probs, torch.float32, (M, k), dev))
 
