@@ -274,8 +274,8 @@ def _prepare_norm(c, g, s):
     s["dw_before"] = empty(torch.float32, K)
     s["dgate"] = None if s["gate"] is None else empty(s["gate"].dtype, *shape)
     if own:  # the workspace that a training program keeps
-        from moe_expert_ffn_amd import megamoe as MM
-        s["workspace"] = torch.empty(MM.megamoe_norm_grad_workspace_bytes(_dims(MM, c)), dtype=torch.uint8, device=DEV)
+        from moe_expert_ffn_amd import half as H
+        s["workspace"] = torch.empty(H.megamoe_norm_grad_workspace_bytes(_dims(c)), dtype=torch.uint8, device=DEV)
     return s
 
 
@@ -283,7 +283,8 @@ def _prepare_norm(c, g, s):
 # one pass
 
 
-def _dims(MM, c):
+def _dims(c):
+    from moe_expert_ffn_amd import megamoe as MM
     return MM.dims(c["M"], c.get("K", 128), c["E"], c["top_k"], c.get("I", 128))
 
 
@@ -293,45 +294,45 @@ def run(s):
     if not own:
         return {"swiglu": _swiglu, "swiglu_grad": _swiglu_grad, "norm": _norm, "norm_grad": _norm_grad,
                 "route_grad": _route_grad}.get(op, _wgrad if op.endswith("wgrad") else _gmm)(s, c)
-    from moe_expert_ffn_amd import megamoe as MM
-    d = _dims(MM, c)
+    from moe_expert_ffn_amd import half as H
+    d = _dims(c)
     if op == "route_grad":
-        MM.megamoe_route_grad(d, s["logits"], s["expert_idx"], s["probs"], s["dprobs"], s["dlogits"],
-                              renormalize=c["renormalize"])
+        H.megamoe_route_grad(d, s["logits"], s["expert_idx"], s["probs"], s["dprobs"], s["dlogits"],
+                             renormalize=c["renormalize"])
         return s["dlogits"]
     if op == "norm":
-        MM.megamoe_norm(d, x=s["x"], rows=s["rows"], expanded_row_idx=s["idx"], w_after=s["w_after"], gate=s["gate"],
-                        alpha=s["alpha"], w_before=s["w_before"], eps=EPS, s=s["s"], r=s["r"], h=s["h"])
+        H.megamoe_norm(d, x=s["x"], rows=s["rows"], expanded_row_idx=s["idx"], w_after=s["w_after"], gate=s["gate"],
+                       alpha=s["alpha"], w_before=s["w_before"], eps=EPS, s=s["s"], r=s["r"], h=s["h"])
         return [s[k] for k in ("s", "r", "h") if s[k] is not None]
     if op == "norm_grad":
-        MM.megamoe_norm_grad(d, s["r"], s["workspace"], dr=s["dr"], dh=s["dh"], expanded_row_idx=s["idx"], s=s["s"],
-                             w_after=s["w_after"], gate=s["gate"], alpha=s["alpha"], w_before=s["w_before"], eps=EPS,
-                             dx=s["dx"], ds=s["ds"], dw_after=s["dw_after"], dw_before=s["dw_before"],
-                             dgate=s["dgate"])
+        H.megamoe_norm_grad(d, s["r"], s["workspace"], dr=s["dr"], dh=s["dh"], expanded_row_idx=s["idx"], s=s["s"],
+                            w_after=s["w_after"], gate=s["gate"], alpha=s["alpha"], w_before=s["w_before"], eps=EPS,
+                            dx=s["dx"], ds=s["ds"], dw_after=s["dw_after"], dw_before=s["dw_before"],
+                            dgate=s["dgate"])
         return [s[k] for k in ("dx", "ds", "dw_after", "dw_before", "dgate") if s[k] is not None]
     route, end = s["sorted_route"], s["expert_cumsum"]
     if op == "swiglu":
-        MM.megamoe_half_swiglu(d, s["c"], route, end, s["y"], probs=s["probs"])
+        H.megamoe_half_swiglu(d, s["c"], route, end, s["y"], probs=s["probs"])
         return s["y"]
     if op == "swiglu_grad":
-        MM.megamoe_half_swiglu_grad(d, s["c"], s["dy"], route, s["expanded_row_idx"], end, s["dc"], probs=s["probs"],
-                                    dprobs=s["dprobs"])
+        H.megamoe_half_swiglu_grad(d, s["c"], s["dy"], route, s["expanded_row_idx"], end, s["dc"], probs=s["probs"],
+                                   dprobs=s["dprobs"])
         return [s["dc"]] + ([s["dprobs"]] if c["weighted"] else [])
     if op == "gmm1":
         if c["act"]:
-            MM.megamoe_half_gmm1_swiglu(d, s["a"], route, end, s["w"], s["y"], probs=s["probs"])
+            H.megamoe_half_gmm1_swiglu(d, s["a"], route, end, s["w"], s["y"], probs=s["probs"])
         else:
-            MM.megamoe_half_gmm1(d, s["a"], route, end, s["w"], s["y"])
+            H.megamoe_half_gmm1(d, s["a"], route, end, s["w"], s["y"])
     elif op == "gmm2":
-        MM.megamoe_half_gmm2(d, s["a"], end, s["w"], s["y"])
+        H.megamoe_half_gmm2(d, s["a"], end, s["w"], s["y"])
     elif op == "gmm1_dgrad":
-        MM.megamoe_half_gmm1_dgrad(d, s["a"], end, s["w"], s["y"])
+        H.megamoe_half_gmm1_dgrad(d, s["a"], end, s["w"], s["y"])
     elif op == "gmm2_dgrad":
-        MM.megamoe_half_gmm2_dgrad(d, s["a"], route, end, s["w"], s["y"])
+        H.megamoe_half_gmm2_dgrad(d, s["a"], route, end, s["w"], s["y"])
     elif op == "gmm1_wgrad":
-        MM.megamoe_half_gmm1_wgrad(d, s["a"], s["b"], route, end, s["dw"])
+        H.megamoe_half_gmm1_wgrad(d, s["a"], s["b"], route, end, s["dw"])
     else:
-        MM.megamoe_half_gmm2_wgrad(d, s["a"], s["b"], route, end, s["dw"])
+        H.megamoe_half_gmm2_wgrad(d, s["a"], s["b"], route, end, s["dw"])
     return s["dw"] if op.endswith("wgrad") else s["y"]
 
 
