@@ -6,8 +6,11 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "../../include/megamoe.h"
+#include "../../include/megamoe/half.h"
+#include "half.hpp"
 #include "kernels.hpp"
 
 
@@ -281,6 +284,54 @@ int check_mxfp4_rows(int64_t rows, int64_t cols) {
         return MEGAMOE_EUNSUPPORTED;
     return MEGAMOE_OK;
 }
+
+bool half_type(int type) { return type == MEGAMOE_FP16 || type == MEGAMOE_BF16; }
+
+// gather: 0, or which operand's rows are token rows read through `route`.
+int run_half_gmm(const megamoe_dims &d, int kind, bool first, const uint16_t *a, const uint16_t *b,
+                 int type, const int32_t *route, int gather, const int32_t *cumsum,
+                 const float *probs, bool swiglu, void *c, int c_type, bool accumulate,
+                 hipStream_t s) {
+    const int inner = first && !swiglu ? 2 * d.I : d.I, wide = first ? 2 * d.I : d.I;
+    HalfGmmParams p{a, b, route, cumsum, probs, c, d.M * d.top_k, d.E, 0, 0, 0, d.top_k,
+                    (uint32_t)(((1ull << 32) + d.top_k - 1) / d.top_k),  // see run_mxfp4_gmm
+                    gather, swiglu, accumulate, c_type};
+    if (kind == kHalfWeights) {
+        p.M = first ? wide : d.K;
+        p.N = first ? d.K : wide;
+    } else {  // the first product and the second's row gradient end in the inner columns
+        const bool to_inner = first == (kind == kHalfProduct);
+        p.N = to_inner ? inner : d.K;
+        p.K = to_inner ? d.K : inner;
+    }
+    return hip_status(launch_half_gmm(p, kind, type, cu_count_current(), s));
+}
+
+// workspace of the 16-bit forward
+struct HalfLayout {
+    size_t err, bcnt, eri, sorted, counts, cumsum, y, g2, total;
+};
+HalfLayout half_layout(const megamoe_dims &d) {
+    const size_t M = d.M, R = M * d.top_k;
+    HalfLayout L;
+    size_t o = 0;
+    L.err = o;    o += align_up(kErrBytes);
+    L.bcnt = o;   o += align_up(route_sort_workspace_bytes((int)R, d.E));
+    L.eri = o;    o += align_up(R * 4);
+    L.sorted = o; o += align_up(R * 4);
+    L.counts = o; o += align_up((size_t)d.E * 4);
+    L.cumsum = o; o += align_up((size_t)d.E * 4);
+    L.y = o;      o += align_up(R * d.I * 2);
+    L.g2 = o;     o += align_up(R * d.K * 2);
+    L.total = o;
+    return L;
+}
+
+bool gate_ok(const megamoe_dims &d, int64_t rows, int64_t cols) {
+    return (rows == 1 || rows == d.M) && (cols == 1 || cols == d.K);
+}
+// a pointer that has to be there and aligned, or has to be missing
+bool given(const void *p, bool wanted) { return wanted ? aligned16(p) : p == nullptr; }
 
 }  // namespace
 
@@ -677,6 +728,305 @@ int megamoe_forward_mxfp4(const megamoe_dims *d, const uint16_t *x, const int32_
     MEGAMOE_TRY(run_mxfp4_gmm(*d, xq, xs, sorted, cumsum, w1q, w1s, nullptr, yq, ys, true, s));
     MEGAMOE_TRY(run_mxfp4_gmm(*d, yq, ys, nullptr, cumsum, w2q, w2s, g2, nullptr, nullptr, false, s));
     return hip_status(launch_unpermute(g2, nullptr, eri, probs, d->M, d->K, d->top_k, out, s));
+}
+
+int megamoe_sort_routes(const megamoe_dims *d, const int32_t *expert_idx, int32_t *eri,
+                        int32_t *sorted_route, int32_t *tokens_per_expert, int32_t *expert_cumsum,
+                        void *ws, size_t ws_bytes, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {expert_idx, eri, sorted_route, tokens_per_expert, expert_cumsum, ws};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (ws_bytes < permute_ws_bytes(*d)) return MEGAMOE_EWORKSPACE;
+    char *w = (char *)ws;
+    return hip_status(launch_route_sort(expert_idx, d->M * d->top_k, d->E, sorted_route, eri,
+                                        tokens_per_expert, expert_cumsum, (int32_t *)w,
+                                        (int32_t *)(w + align_up(kErrBytes)), (hipStream_t)stream));
+}
+
+int megamoe_half_gmm1(const megamoe_dims *d, const uint16_t *x, int type,
+                      const int32_t *sorted_route, const int32_t *expert_cumsum,
+                      const uint16_t *w1, uint16_t *c, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {x, sorted_route, expert_cumsum, w1, c};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfProduct, true, x, w1, type, sorted_route, 1, expert_cumsum,
+                        nullptr, false, c, type, false, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm1_swiglu(const megamoe_dims *d, const uint16_t *x, int type,
+                             const int32_t *sorted_route, const int32_t *expert_cumsum,
+                             const float *probs, const uint16_t *w1, uint16_t *y, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {x, sorted_route, expert_cumsum, w1, y};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if ((probs && !aligned16(probs)) || !half_type(type)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfProduct, true, x, w1, type, sorted_route, 1, expert_cumsum, probs,
+                        true, y, type, false, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm2(const megamoe_dims *d, const uint16_t *y, int type,
+                      const int32_t *expert_cumsum, const uint16_t *w2, uint16_t *gmm2_out,
+                      void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {y, expert_cumsum, w2, gmm2_out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfProduct, false, y, w2, type, nullptr, 0, expert_cumsum, nullptr,
+                        false, gmm2_out, type, false, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm1_dgrad(const megamoe_dims *d, const uint16_t *dc, int type,
+                            const int32_t *expert_cumsum, const uint16_t *w1, uint16_t *dx_rows,
+                            void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {dc, expert_cumsum, w1, dx_rows};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfRows, true, dc, w1, type, nullptr, 0, expert_cumsum, nullptr,
+                        false, dx_rows, type, false, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm2_dgrad(const megamoe_dims *d, const uint16_t *dout, int type,
+                            const int32_t *sorted_route, const int32_t *expert_cumsum,
+                            const uint16_t *w2, uint16_t *dy, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {dout, sorted_route, expert_cumsum, w2, dy};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfRows, false, dout, w2, type, sorted_route, 1, expert_cumsum,
+                        nullptr, false, dy, type, false, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm1_wgrad(const megamoe_dims *d, const uint16_t *dc, const uint16_t *x, int type,
+                            const int32_t *sorted_route, const int32_t *expert_cumsum, void *dw1,
+                            int dw_type, int accumulate, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {dc, x, sorted_route, expert_cumsum, dw1};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type) || (dw_type != type && dw_type != MEGAMOE_FP32)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfWeights, true, dc, x, type, sorted_route, 2, expert_cumsum,
+                        nullptr, false, dw1, dw_type, accumulate != 0, (hipStream_t)stream);
+}
+
+int megamoe_half_gmm2_wgrad(const megamoe_dims *d, const uint16_t *dout, const uint16_t *y,
+                            int type, const int32_t *sorted_route, const int32_t *expert_cumsum,
+                            void *dw2, int dw_type, int accumulate, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {dout, y, sorted_route, expert_cumsum, dw2};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type) || (dw_type != type && dw_type != MEGAMOE_FP32)) return MEGAMOE_EINVAL;
+    return run_half_gmm(*d, kHalfWeights, false, dout, y, type, sorted_route, 1, expert_cumsum,
+                        nullptr, false, dw2, dw_type, accumulate != 0, (hipStream_t)stream);
+}
+
+int megamoe_half_swiglu(const megamoe_dims *d, const uint16_t *c, int type,
+                        const int32_t *sorted_route, const int32_t *expert_cumsum,
+                        const float *probs, uint16_t *y, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {c, sorted_route, expert_cumsum, y};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if ((probs && !aligned16(probs)) || !half_type(type)) return MEGAMOE_EINVAL;
+    HalfSwigluParams p{};
+    p.c = c;
+    p.route = sorted_route;
+    p.cumsum = expert_cumsum;
+    p.probs = probs;
+    p.y = y;
+    p.R = d->M * d->top_k;
+    p.E = d->E;
+    p.I = d->I;
+    return hip_status(launch_half_swiglu(p, type, false, (hipStream_t)stream));
+}
+
+int megamoe_half_swiglu_grad(const megamoe_dims *d, const uint16_t *c, const uint16_t *dy,
+                             int type, const int32_t *sorted_route,
+                             const int32_t *expanded_row_idx, const int32_t *expert_cumsum,
+                             const float *probs, uint16_t *dc, float *dprobs, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {c, dy, sorted_route, expanded_row_idx, expert_cumsum, dc};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if ((probs && !aligned16(probs)) || (dprobs && !aligned16(dprobs)) || !half_type(type))
+        return MEGAMOE_EINVAL;
+    HalfSwigluParams p{};
+    p.c = c;
+    p.dy = dy;
+    p.route = sorted_route;
+    p.row_of = expanded_row_idx;
+    p.cumsum = expert_cumsum;
+    p.probs = probs;
+    p.dc = dc;
+    p.dprobs = dprobs;
+    p.R = d->M * d->top_k;
+    p.E = d->E;
+    p.I = d->I;
+    return hip_status(launch_half_swiglu(p, type, true, (hipStream_t)stream));
+}
+
+int megamoe_norm(const megamoe_dims *d, const void *x, int x_type, const void *rows, int rows_type,
+                 const int32_t *expanded_row_idx, const float *w_after, const void *gate,
+                 int gate_type, int64_t gate_rows, int64_t gate_cols, float alpha,
+                 const float *w_before, float eps, void *s, void *r, void *h, int h_type,
+                 void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *nullable[] = {x, rows, expanded_row_idx, w_after, gate, w_before, s, r, h};
+    for (const void *p : nullable)
+        if (p && !aligned16(p)) return MEGAMOE_EINVAL;
+    if ((!x && !rows) || (!s && !r && !h)) return MEGAMOE_EINVAL;
+    if (!rows && (expanded_row_idx || w_after || gate || s)) return MEGAMOE_EINVAL;
+    if ((h == nullptr) != (w_before == nullptr)) return MEGAMOE_EINVAL;
+    if (!type_ok(x_type) || !type_ok(rows_type) || !type_ok(h_type)) return MEGAMOE_EINVAL;
+    if (gate && (!type_ok(gate_type) || !gate_ok(*d, gate_rows, gate_cols))) return MEGAMOE_EINVAL;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(alpha)) return MEGAMOE_EINVAL;
+    NormParams p{};
+    p.x = x;
+    p.rows = rows;
+    p.row_of = expanded_row_idx;
+    p.w_after = w_after;
+    p.w_before = w_before;
+    p.gate = gate;
+    p.s = s;
+    p.r = r;
+    p.h = h;
+    p.M = d->M;
+    p.K = d->K;
+    p.top_k = d->top_k;
+    p.R = d->M * d->top_k;
+    p.gate_type = gate_type;
+    p.gate_rows = (int)gate_rows;
+    p.gate_cols = (int)gate_cols;
+    p.h_type = h_type;
+    p.alpha = alpha;
+    p.eps = eps;
+    return hip_status(launch_norm(p, x_type, rows_type, false, (hipStream_t)stream));
+}
+
+int megamoe_norm_grad_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    if (!bytes) return MEGAMOE_EINVAL;
+    *bytes = (size_t)3 * norm_grad_groups(d->M) * d->K * sizeof(float);
+    return MEGAMOE_OK;
+}
+
+int megamoe_norm_grad(const megamoe_dims *d, const void *dr, const void *r, int x_type,
+                      const void *dh, int h_type, const int32_t *expanded_row_idx, const void *s,
+                      int rows_type, const float *w_after, const void *gate, int gate_type,
+                      int64_t gate_rows, int64_t gate_cols, float alpha, const float *w_before,
+                      float eps, void *dx, void *ds, float *dw_after, float *dw_before,
+                      void *dgate, void *ws, size_t ws_bytes, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    if (!aligned16(dx) || !aligned16(ws) || (dr && !aligned16(dr)) || (!dr && !dh))
+        return MEGAMOE_EINVAL;
+    if (expanded_row_idx && (!aligned16(expanded_row_idx) || !dh)) return MEGAMOE_EINVAL;
+    const bool before = w_before != nullptr, block = s != nullptr;
+    if (!given(w_before, before) || !given(r, before) || !given(dh, before) ||
+        !given(dw_before, before))
+        return MEGAMOE_EINVAL;
+    if (!given(s, block) || !given(ds, block)) return MEGAMOE_EINVAL;
+    const bool after = w_after != nullptr, gated = gate != nullptr;
+    if ((after || gated) && !block) return MEGAMOE_EINVAL;
+    if (!given(w_after, after) || !given(dw_after, after) || !given(gate, gated) ||
+        !given(dgate, gated))
+        return MEGAMOE_EINVAL;
+    if (!type_ok(x_type) || !type_ok(rows_type) || !type_ok(h_type)) return MEGAMOE_EINVAL;
+    if (gated && (!type_ok(gate_type) || !gate_ok(*d, gate_rows, gate_cols))) return MEGAMOE_EINVAL;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(alpha)) return MEGAMOE_EINVAL;
+    size_t need = 0;
+    MEGAMOE_TRY(megamoe_norm_grad_workspace_bytes(d, &need));
+    if (ws_bytes < need) return MEGAMOE_EWORKSPACE;
+    NormParams p{};
+    p.row_of = expanded_row_idx;
+    p.w_after = w_after;
+    p.w_before = w_before;
+    p.gate = gate;
+    p.s = const_cast<void *>(s);
+    p.r = const_cast<void *>(r);
+    p.h = const_cast<void *>(dh);
+    p.dr = dr;
+    p.dx = dx;
+    p.ds = ds;
+    p.dgate = dgate;
+    p.dw_after = dw_after;
+    p.dw_before = dw_before;
+    p.part = (float *)ws;
+    p.M = d->M;
+    p.K = d->K;
+    p.top_k = d->top_k;
+    p.R = d->M * d->top_k;
+    p.gate_type = gate_type;
+    p.gate_rows = (int)gate_rows;
+    p.gate_cols = (int)gate_cols;
+    p.h_type = h_type;
+    p.alpha = alpha;
+    p.eps = eps;
+    return hip_status(launch_norm(p, x_type, rows_type, true, (hipStream_t)stream));
+}
+
+int megamoe_route_grad(const megamoe_dims *d, const void *logits, int logits_type,
+                       const float *bias, int renormalize, const int32_t *expert_idx,
+                       const float *probs, const float *dprobs, void *dlogits, void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {logits, expert_idx, probs, dprobs, dlogits};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if ((bias && !aligned16(bias)) || !type_ok(logits_type)) return MEGAMOE_EINVAL;
+    const RouteGradParams p{logits, bias, expert_idx, probs, dprobs, dlogits,
+                            d->M, d->E, d->top_k, renormalize != 0};
+    return hip_status(launch_route_grad(p, logits_type, (hipStream_t)stream));
+}
+
+int megamoe_half_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    if (!bytes) return MEGAMOE_EINVAL;
+    *bytes = half_layout(*d).total;
+    return MEGAMOE_OK;
+}
+
+int megamoe_forward_half(const megamoe_dims *d, const uint16_t *x, int type,
+                         const int32_t *expert_idx, const float *probs, const uint16_t *w1,
+                         const uint16_t *w2, uint16_t *out, void *ws, size_t ws_bytes,
+                         void *stream) {
+    MEGAMOE_TRY(megamoe_check_dims(d));
+    const void *ptrs[] = {x, expert_idx, probs, w1, w2, out, ws};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MEGAMOE_EINVAL;
+    if (!half_type(type)) return MEGAMOE_EINVAL;
+    const HalfLayout L = half_layout(*d);
+    if (ws_bytes < L.total) return MEGAMOE_EWORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    char *base = (char *)ws;
+    int32_t *eri = (int32_t *)(base + L.eri);
+    int32_t *sorted = (int32_t *)(base + L.sorted);
+    int32_t *cumsum = (int32_t *)(base + L.cumsum);
+    uint16_t *y = (uint16_t *)(base + L.y), *g2 = (uint16_t *)(base + L.g2);
+    MEGAMOE_TRY(hip_status(launch_route_sort(expert_idx, d->M * d->top_k, d->E, sorted, eri,
+                                             (int32_t *)(base + L.counts), cumsum,
+                                             (int32_t *)(base + L.err),
+                                             (int32_t *)(base + L.bcnt), s)));
+    MEGAMOE_TRY(run_half_gmm(*d, kHalfProduct, true, x, w1, type, sorted, 1, cumsum, probs, true, y,
+                             type, false, s));
+    MEGAMOE_TRY(run_half_gmm(*d, kHalfProduct, false, y, w2, type, nullptr, 0, cumsum, nullptr,
+                             false, g2, type, false, s));
+    NormParams p{};  // no norm: the rows' sum alone
+    p.rows = g2;
+    p.row_of = eri;
+    p.r = out;
+    p.M = d->M;
+    p.K = d->K;
+    p.top_k = d->top_k;
+    p.R = d->M * d->top_k;
+    p.alpha = p.eps = 1.0f;
+    return hip_status(launch_norm(p, type, type, false, s));
 }
 
 int megamoe_set_overlap(int mode) {

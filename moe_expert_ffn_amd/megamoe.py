@@ -118,6 +118,28 @@ def load() -> ctypes.CDLL:
     L.megamoe_mxfp4_workspace_bytes.restype = i32
     L.megamoe_forward_mxfp4.argtypes = [D, P, P, P, P, P, P, P, P, P, sz, P]
     L.megamoe_forward_mxfp4.restype = i32
+    f32 = ctypes.c_float
+    for name, args in {
+        "megamoe_sort_routes": [D, P, P, P, P, P, P, sz, P],
+        "megamoe_half_gmm1": [D, P, i32, P, P, P, P, P],
+        "megamoe_half_gmm1_swiglu": [D, P, i32, P, P, P, P, P, P],
+        "megamoe_half_gmm2": [D, P, i32, P, P, P, P],
+        "megamoe_half_gmm1_dgrad": [D, P, i32, P, P, P, P],
+        "megamoe_half_gmm2_dgrad": [D, P, i32, P, P, P, P, P],
+        "megamoe_half_gmm1_wgrad": [D, P, P, i32, P, P, P, i32, i32, P],
+        "megamoe_half_gmm2_wgrad": [D, P, P, i32, P, P, P, i32, i32, P],
+        "megamoe_half_swiglu": [D, P, i32, P, P, P, P, P],
+        "megamoe_half_swiglu_grad": [D, P, P, i32, P, P, P, P, P, P, P],
+        "megamoe_norm": [D, P, i32, P, i32, P, P, P, i32, i64, i64, f32, P, f32, P, P, P, i32, P],
+        "megamoe_norm_grad_workspace_bytes": [D, psz],
+        "megamoe_norm_grad": [D, P, P, i32, P, i32, P, P, i32, P, P, i32, i64, i64, f32, P, f32,
+                              P, P, P, P, P, P, sz, P],
+        "megamoe_route_grad": [D, P, i32, P, i32, P, P, P, P, P],
+        "megamoe_half_workspace_bytes": [D, psz],
+        "megamoe_forward_half": [D, P, i32, P, P, P, P, P, P, sz, P],
+    }.items():
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, i32
     _lib = L
     return L
 
