@@ -2,129 +2,711 @@
 // sections 3 and 5 of the pto-isa MegaMoE overview page, with unquantised experts).
 //
 // For the rows d of expert e's group, sums in fp32 on the matrix cores:
-//   product   c[d, n] = sum_k a[d, k] w[e, n, k]      (w: rows over the reduction)
-//   rows      c[d, n] = sum_k a[d, k] w[e, k, n]      (the gradient of a product's rows)
+//   product   c[d, n] = sum_k a[d, k] b[e, n, k]
+//   rows      c[d, n] = sum_k a[d, k] b[e, k, n]      (the gradient of a product's rows)
 //   weights   c[e, m, n] = sum_d a[d, m] b[d, n]      (the gradient of its weights)
-// The rows of a or b may be gathered: row d is row route[d] / top_k of the array.
+// The rows of a or b may be gathered: row d is row route[d] / top_k of the array.  A product
+// may end in SwiGLU: columns n and N + n of b meet in the same lane's accumulators.
+#include <type_traits>
+
 #include "common.hpp"
+#include "dma.hpp"
 #include "element.hpp"
 #include "half.hpp"
-#include "swiglu_row.hpp"
 
 namespace megamoe {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ int half_row_end(const HalfGmmParams &p, int e) {
+__device__ __forceinline__ int hg_row_end(const HalfGmmParams &p, int e) {
     const int v = e >= 0 ? p.cumsum[e] : 0;
     return v < 0 ? 0 : v > p.R ? p.R : v;
 }
 
-__device__ __forceinline__ uint32_t half_row(const HalfGmmParams &p, bool gathered, int d) {
-    if (!gathered) return d;
-    const int v = p.route[d];
-    const uint32_t u = v < 0 ? 0 : v < p.R ? v : p.R - 1;
+// The token of a sorted route: what lies past the valid rows stays in bounds.
+__device__ __forceinline__ uint32_t hg_route(const HalfGmmParams &p, int v) { return v < 0 ? 0 : v < p.R ? v : p.R - 1; }
+__device__ __forceinline__ uint32_t hg_token(const HalfGmmParams &p, int v) {
+    const uint32_t u = hg_route(p, v);
     return p.top_k == 1 ? u : __umulhi(u, p.top_k_inv);
 }
 
+// 32 x 32 x 16 with the columns' operand first: lane l holds output row l & 31 and the columns
+// 8 q + 4 (l >> 5) + 0..3, q = 0..3.  Of either operand lane l has row l & 31 and 8 (l >> 5) + 0..7 of the reduction.
 template <int T>
-__device__ __forceinline__ v16f half_mfma(uint4 w, uint4 a, v16f acc) {
+__device__ __forceinline__ v16f hg_mfma(v4i w, v4i a, v16f acc) {
     if constexpr (T == kBf16)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, a), acc, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, a), acc, 0, 0, 0);
 }
 
-// A tile of 64 by 64 a workgroup, 32 by 32 a wave, 32 of the reduction at a time through LDS.
-constexpr int kHalfTile = 64, kHalfK = 32, kHalfPad = 8;
+// ---------------------------------------------------------------------------
+// Tiles of 256 rows by 256 columns, four waves to a tile and one to a SIMD, each multiplying all of
+// its rows by 64 of its columns: 8 x 2 fragments of 32 x 32 sums fill half of the register file, and the time of a
+// tile follows its live rows in steps of 64.
+//
+// A stage is 64 of the reduction, copied asynchronously into one of two slots in LDS, 128 bytes (a whole
+// cache line) at a time.  An operand lies there in one of two ways:
+//   along    its rows run along the reduction: [256 rows][128 bytes], fragments read 16 bytes a lane;
+//   across   its rows run across it: [4 panels][64 of the reduction][64 columns], fragments read by the
+//            transposing LDS load, which gives a lane four values of one column.
+// Either way the 16-byte pieces are placed so that a fragment's reads meet every LDS bank equally often.
+//
+// A wave multiplies by columns that it has copied itself, and has all of a stage's in registers when the stage
+// begins: those of the stage after the next are copied from then on.  The barrier between two stages lies
+// before the last rows of the first are multiplied: they are in registers by then, so behind it the rows
+// of the stage after the next are copied, and the first fragments of the next one are read.
+//
+// The grid is persistent, and the copies run two stages ahead of the products through the workgroup's
+// tiles, so that a tile's first stages are there when the tile before has been rounded and stored.
+constexpr int kHgThreads = 256;
+constexpr int kHgE = 256;
+constexpr int kHgTile = 256, kHgK = 64;
+constexpr int kHgOperand = kHgTile * kHgK * 2;  // bytes of an operand's stage
+constexpr int kHgList = 64;                     // tiles looked up ahead, half of them at a time
+constexpr int kHgRing = 8;                      // stages whose routes are kept (weights' gradients)
 
-template <int KIND, int T>
-__global__ __launch_bounds__(256) void half_gmm_kernel(HalfGmmParams p, int row_blocks) {
-    __shared__ __align__(16) uint16_t s_a[kHalfTile][kHalfK + kHalfPad], s_b[2][kHalfTile][kHalfK + kHalfPad];
-    const int e = blockIdx.z, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int first = half_row_end(p, e - 1), rows = max(0, half_row_end(p, e) - first);
-    const int n0 = blockIdx.y * kHalfTile;
-    const bool swiglu = KIND == kHalfProduct && p.swiglu;
-    const int m_end = KIND == kHalfWeights ? p.M : rows, red = KIND == kHalfWeights ? rows : p.K;
-    const int wn = swiglu ? 2 * p.N : p.N;
-    for (int mb = blockIdx.x; mb * kHalfTile < m_end; mb += row_blocks) {
-        const int m0 = mb * kHalfTile;
-        v16f acc[2] = {};
-        for (int k0 = 0; k0 < red; k0 += kHalfK) {
-            __syncthreads();
-            // rows with the reduction along them, 8 elements a thread; or the other way round
-            auto stage = [&](uint16_t(*s)[kHalfK + kHalfPad], bool along, auto address) {
-                if (along) {
-                    const int r = tid >> 2, k = (tid & 3) * 8;
-                    *reinterpret_cast<uint4 *>(&s[r][k]) = *reinterpret_cast<const uint4 *>(address(r, k0 + k));
-                } else {
-                    const int k = tid >> 3, r = (tid & 7) * 8;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (k0 + k < red) v = *reinterpret_cast<const uint4 *>(address(r, k0 + k));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    for (int j = 0; j < 8; ++j) s[r + j][k] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-                }
-            };
-            if (KIND == kHalfWeights) {
-                stage(s_a, false, [&](int r, int k) {
-                    return p.a + (size_t)half_row(p, p.gather == 1, first + k) * p.M + min(m0 + r, p.M - 8);
-                });
-                stage(s_b[0], false, [&](int r, int k) {
-                    return p.b + (size_t)half_row(p, p.gather == 2, first + k) * p.N + min(n0 + r, p.N - 8);
-                });
-            } else {
-                stage(s_a, true, [&](int r, int k) {
-                    return p.a + (size_t)half_row(p, p.gather == 1, first + min(m0 + r, rows - 1)) * p.K + k;
-                });
-                for (int f = 0; f < (swiglu ? 2 : 1); ++f)
-                    stage(s_b[f], KIND == kHalfProduct, [&](int r, int k) {
-                        const uint16_t *w = p.b + (size_t)e * wn * p.K;
-                        return KIND == kHalfProduct ? w + (size_t)(f * p.N + min(n0 + r, p.N - 1)) * p.K + k
-                                                    : w + (size_t)k * p.N + min(n0 + r, p.N - 8);
-                    });
-            }
-            __syncthreads();
-            const int r = lane & 31, g = lane >> 5;
+template <int KIND_, int T_, bool SWIGLU_>
+struct HgGeom {
+    static constexpr int KIND = KIND_, T = T_;
+    static constexpr bool SWIGLU = SWIGLU_;
+    static constexpr bool WEIGHTS = KIND == kHalfWeights;
+    static constexpr bool A_ACROSS = WEIGHTS, B_ACROSS = KIND != kHalfProduct;
+    static constexpr int F = SWIGLU ? 2 : 1;
+    static constexpr int COLS = kHgTile / F;  // output columns of a tile
+    static constexpr int J = 2 / F;           // fragments of 32 columns that a wave stores
+};
+
+struct HgTile {
+    int e, row0, rows, nblk;  // first output row and how many, block of columns
+    int first, red;           // weights: the group's first row; the reduction's length
+};
+
+struct HgSchedule {
+    int pre[kHgE + 1];  // products: tiles of the experts before e
+    int first[kHgE], rows[kHgE];
+    int order[kHgE];    // weights: experts, most rows first
+    int total;
+};
+
+// Products: tiles by expert, column block and row block, an expert's rows split evenly over its row blocks in
+// units of 32.  Weights: every expert has as many tiles, those of the largest groups first.
+template <typename G>
+__device__ __forceinline__ void hg_schedule(const HalfGmmParams &p, int *s_w, HgSchedule &s) {
+    const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
+    const int first = e < p.E ? hg_row_end(p, e - 1) : 0;
+    const int rows = e < p.E ? max(0, hg_row_end(p, e) - first) : 0;
+    s.first[e] = first;
+    s.rows[e] = rows;
+    if constexpr (G::WEIGHTS) {
+        __syncthreads();
+        int rank = 0;
+        for (int i = 0; i < p.E; ++i) {
+            const int other = s.rows[i];
+            rank += other > rows || (other == rows && i < e);
+        }
+        if (e < p.E) s.order[rank] = e;
+        if (e == 0)
+            s.total = p.E * ((p.M + kHgTile - 1) / kHgTile) * ((p.N + kHgTile - 1) / kHgTile);
+    } else {
+        const int tiles = (rows + kHgTile - 1) / kHgTile * ((p.N + G::COLS - 1) / G::COLS);
+        const int incl = wave_inclusive_scan(tiles);
+        if (lane == kWave - 1) s_w[wave] = incl;
+        __syncthreads();
+        int pre = incl - tiles;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint4 a = *reinterpret_cast<const uint4 *>(&s_a[(wave >> 1) * 32 + r][16 * h + 8 * g]);
-                for (int f = 0; f < (swiglu ? 2 : 1); ++f)
-                    acc[f] = half_mfma<T>(*reinterpret_cast<const uint4 *>(&s_b[f][(wave & 1) * 32 + r][16 * h + 8 * g]), a, acc[f]);
+        for (int w = 0; w < 4; ++w) pre += w < wave ? s_w[w] : 0;
+        s.pre[e] = pre;  // experts past E have no tiles: pre is the total
+        if (e == kHgE - 1) s.pre[kHgE] = s.total = pre + tiles;
+    }
+    __syncthreads();
+}
+
+template <typename G>
+__device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgSchedule &s, int t) {  // t < total
+    if constexpr (G::WEIGHTS) {
+        const int mb = (p.M + kHgTile - 1) / kHgTile, nb = (p.N + kHgTile - 1) / kHgTile;
+        const int e = s.order[t / (mb * nb)], local = t % (mb * nb), m0 = local % mb * kHgTile;
+        return HgTile{e, m0, min(kHgTile, p.M - m0), local / mb, s.first[e], s.rows[e]};
+    } else {
+        int lo = 0, hi = kHgE - 1;  // the first expert that ends after t
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s.pre[mid + 1] > t) hi = mid;
+            else lo = mid + 1;
+        }
+        const int rows = s.rows[lo], local = t - s.pre[lo];
+        const int mb = (rows + kHgTile - 1) / kHgTile, m = local % mb;
+        const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
+        const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
+        return HgTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, local / mb, 0, p.K};
+    }
+}
+__device__ __forceinline__ HgTile hg_uniform(const HgTile &x) {
+    return HgTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.row0),
+                  __builtin_amdgcn_readfirstlane(x.rows), __builtin_amdgcn_readfirstlane(x.nblk),
+                  __builtin_amdgcn_readfirstlane(x.first), __builtin_amdgcn_readfirstlane(x.red)};
+}
+
+struct HgLds {
+    uint8_t *data;
+    uint32_t data_at;  // its LDS address
+    int32_t *route;    // products: [2][256] routes of a tile's rows; weights: [kHgRing][64] routes of a stage
+    float *weight;     // products with SwiGLU: [3][256] weights of a tile's rows
+    uint32_t route_at, weight_at;
+};
+
+// 16-byte piece c of a row that lies along the reduction: its place.  LDS has 64 banks, two rows; reads of one
+// piece of 16 rows in the order of the lanes meet each bank once.
+__device__ __forceinline__ int hg_swz(int row, int c) { return c ^ (row >> 1 & 7); }
+
+// One 16-byte piece a lane into LDS through a buffer: 0 where voff is not within it.
+__device__ __forceinline__ void dma16_buffer(v4i rsrc, uint32_t voff, uint32_t lds_base) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds"
+        :
+        : "s"(lds_base), "v"(voff), "s"(rsrc)
+        : "memory", "m0");
+}
+__device__ __forceinline__ v4i hg_buffer(const void *base, uint32_t bytes) {
+    const uint64_t v = (uint64_t)base;
+    return v4i{(int)__builtin_amdgcn_readfirstlane((uint32_t)v), (int)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)),
+               (int)__builtin_amdgcn_readfirstlane(bytes), 0x00027000};
+}
+
+// Copies of a stage: eight of each operand a wave.  A wave's pieces of an operand are 64 of its rows (along) or a
+// panel of 64 of its columns (across).
+template <typename G>
+struct HgCopies {
+    uint32_t va[8], vb[8];  // byte offsets of a lane's pieces (products: of the tile; weights: of a stage)
+    const uint8_t *a, *b;   // products: where they count from
+    v4i ra, rb;             // weights: the same, with bounds
+    uint32_t ca, cb;        // weights: the lane's columns
+    int first, red, e;
+};
+
+// column piece of a lane in its panel of columns from n0, of n that are a multiple of 128
+__device__ __forceinline__ uint32_t hg_across_column(int n0, int n) {
+    const int lane = threadIdx.x & 63, c = lane & 7;
+    // halves of a panel's rows change places with bit 1 of the row, which is bit 4 of the lane: see hg_across
+    int col = n0 + ((c >> 2) ^ (lane >> 4 & 1)) * 32 + (c & 3) * 8;
+    if (col >= n) col = n - 64 + (col & 63);
+    return 2 * (uint32_t)col;
+}
+
+template <typename G>
+__device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t, int k, const HgLds &l, HgCopies<G> &c) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (G::WEIGHTS) {
+        c.first = t.first;
+        c.red = t.red;
+        c.ca = hg_across_column(t.row0 + wave * 64, p.M);
+        c.cb = hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
+        // of rows past the group nothing is read: their offsets are not within the buffer
+        const uint32_t la = 2 * p.M, lb = 2 * p.N, tokens = p.R / p.top_k;
+        c.ra = p.gather == 1 ? hg_buffer(p.a, tokens * la) : hg_buffer(p.a + (size_t)t.first * p.M, t.red * la);
+        c.rb = p.gather == 2 ? hg_buffer(p.b, tokens * lb) : hg_buffer(p.b + (size_t)t.first * p.N, t.red * lb);
+    } else {
+        const uint32_t la = 2 * p.K;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = (wave * 8 + i) * 8 + (lane >> 3), piece = hg_swz(r, lane & 7) * 16;
+            const int live = min(r, t.rows - 1);
+            const uint32_t row = p.gather ? hg_token(p, l.route[(k & 1) * kHgTile + live]) : (uint32_t)(t.row0 + live);
+            c.va[i] = row * la + piece;
+            if constexpr (G::B_ACROSS) {
+                c.vb[i] = (uint32_t)(8 * i + (lane >> 3)) * (2 * p.N) + hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
+            } else {
+                // with SwiGLU a wave's columns are 32 for silu and the 32 of the gate that go with them
+                const int w = r >> 6, in = r & 63;
+                const int col = t.nblk * G::COLS + (G::SWIGLU ? 32 * w + (in & 31) : r);
+                c.vb[i] = (uint32_t)(min(col, p.N - 1) + (G::SWIGLU && in >= 32 ? p.N : 0)) * la + piece;
             }
         }
-        // lane l holds row l & 31, columns 8 q + 4 (l >> 5) + 0..3
-        const int row = m0 + (wave >> 1) * 32 + (lane & 31);
-        if (row >= m_end) continue;
-        float weight = 1.0f;
-        if (swiglu && p.probs) {
-            const int v = p.route[first + row];
-            weight = p.probs[v < 0 ? 0 : v < p.R ? v : p.R - 1];
-        }
-        const size_t out = KIND == kHalfWeights ? (size_t)e * p.M + row : (size_t)first + row;
-        for (int q = 0; q < 4; ++q)
-            for (int v = 0; v < 4; ++v) {
-                const int n = n0 + (wave & 1) * 32 + 8 * q + 4 * (lane >> 5) + v;
-                if (n >= p.N) continue;
-                float y = swiglu ? weight * silu_times(acc[0][4 * q + v], acc[1][4 * q + v]) : acc[0][4 * q + v];
-                if (KIND == kHalfWeights && p.accumulate) y += load_value(p.c, p.c_type, out * p.N + n);
-                store_value(p.c, p.c_type, out * p.N + n, y);
-            }
+        c.a = uniform_ptr((const uint8_t *)p.a);
+        c.b = uniform_ptr((const uint8_t *)(p.b + (size_t)t.e * G::F * p.N * p.K));
     }
 }
 
+// weights: offsets of the pieces of stage s, one operand
+template <typename G>
+__device__ __forceinline__ void hg_stage_rows(const HalfGmmParams &p, const HgCopies<G> &c, const HgLds &l, int s, int ring,
+                                              bool gathered, uint32_t ld, uint32_t col, uint32_t (&v)[8]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * i + (lane >> 3), d = s * kHgK + r;
+        const uint32_t row = gathered ? hg_token(p, l.route[ring * kHgK + r]) : (uint32_t)d;
+        v[i] = d < c.red ? row * ld + col : 0xffffff00u;  // an array has at most so many bytes
+    }
+}
+
+template <typename G>
+struct HgIssue {  // the copies of one operand's stage s into slot `slot`
+    const HgCopies<G> &c;
+    const uint32_t (&v)[8];
+    const uint8_t *base;
+    v4i rsrc;
+    uint32_t at;
+    bool nt;
+    __device__ __forceinline__ HgIssue(const HalfGmmParams &p, const HgCopies<G> &c_, const HgLds &l, bool b, int s, int slot)
+        : c(c_), v(b ? c_.vb : c_.va), nt(b) {
+        at = l.data_at + (2 * slot + b) * kHgOperand + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 8192;
+        if constexpr (G::WEIGHTS) rsrc = b ? c.rb : c.ra;
+        else if (!b || !G::B_ACROSS) base = uniform_ptr((b ? c.b : c.a) + s * 128);
+        else base = uniform_ptr(c.b + (size_t)s * kHgK * (2 * p.N));
+    }
+    __device__ __forceinline__ void copy(int i) const {
+        if constexpr (G::WEIGHTS) dma16_buffer(rsrc, v[i], at + i * 1024);
+        else if (nt) dma16_nt(base, v[i], at + i * 1024);
+        else dma16(base, v[i], at + i * 1024);
+    }
+};
+template <typename I>
+__device__ __forceinline__ void hg_all(const I &issue) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue.copy(i);
+}
+
+// Fragments of an operand in LDS.
+template <bool ACROSS>
+struct HgRead {
+    const uint8_t *at;
+    int place[4];  // along: of the lane's piece of each step of 16
+    int half[2];   // across: of the halves of a panel
+    __device__ __forceinline__ HgRead() {}
+    __device__ __forceinline__ void lane_places() {
+        const int lane = threadIdx.x & 63;
+        if constexpr (ACROSS) {
+            // rows (lane & 15) >> 2 and 8 (lane >> 5) on, columns 16 (lane >> 4 & 1) + 4 (lane & 3) + 0..3
+            const int swap = lane >> 3 & 1;  // bit 1 of the row
+            const int in = ((lane & 15) >> 2) * 128 + (lane >> 5) * 1024 + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+            half[0] = in + swap * 64;
+            half[1] = in + (swap ^ 1) * 64;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) place[h] = (lane & 31) * 128 + hg_swz(lane & 31, 2 * h + (lane >> 5)) * 16;
+        }
+    }
+    // fragment f of 32 rows or columns, step h
+    __device__ __forceinline__ void read(int f, int h, v4i &v) const {
+        if constexpr (ACROSS) {
+            typedef __attribute__((address_space(3))) v4s *P;
+            const uint8_t *q = at + half[f & 1] + (f >> 1) * 8192 + h * 2048;
+            const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q));
+            const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 512)));
+            v = v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+        } else {
+            v = *reinterpret_cast<const v4i *>(at + f * 4096 + place[h]);
+        }
+    }
+};
+
+// One sum out of the accumulation registers.  (Left to the compiler, all 256 are copied
+// at once and other values spill.)
+__device__ __forceinline__ float hg_sum(float a) {
+    float v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+    return v;
+}
+
+// silu(u) * g for a result that is rounded to 16 bits: the reciprocal's last ulp is not corrected
+__device__ __forceinline__ float hg_silu_times(float u, float g) {
+    const float d = __builtin_amdgcn_exp2f(u * -1.4426950408889634f) + 1.0f;
+    return u * __builtin_amdgcn_rcpf(d) * g;
+}
+
+// Where the copies are: stage s of the workgroup's tile k.
+struct HgCursor {
+    int k, s, ns;
+    HgTile t;
+};
+
+template <typename G>
+struct HgRun {
+    const HalfGmmParams &p;
+    const HgLds &l;
+    const HgTile *list;
+    int n;              // tiles of this workgroup
+    HgCursor ahead;     // the next stage to copy
+    HgCursor routes;    // weights: the next stage whose routes are copied
+    HgCopies<G> c;
+    int stage, total;   // of all of the workgroup's: the one that is multiplied next, and how many there are
+    int stores;         // at least 4 J times as many stores have been made since the last copies
+    HgRead<G::A_ACROSS> ra;
+    HgRead<G::B_ACROSS> rb;
+
+    __device__ __forceinline__ HgTile tile(int k) const { return hg_uniform(list[k & (kHgList - 1)]); }
+    __device__ __forceinline__ void seek(HgCursor &x) const {  // the first stage of tile x.k
+        x.s = 0;
+        x.t = tile(x.k);  // past the last tile what the list happens to hold, which nobody copies
+        x.ns = (x.t.red + kHgK - 1) / kHgK;
+    }
+    __device__ __forceinline__ void step(HgCursor &x) const {
+        if (++x.s < x.ns) return;
+        ++x.k;
+        seek(x);
+    }
+    // products: the routes of tile k's rows; weights: those of a stage
+    __device__ __forceinline__ void fetch_tile_routes(int k) const {
+        if (G::WEIGHTS || !p.route || k >= n) return;
+        const HgTile t = tile(k);
+        const int tid = threadIdx.x;
+        dma4(p.route + t.row0 + min(tid, t.rows - 1),
+             __builtin_amdgcn_readfirstlane(l.route_at + ((k & 1) * kHgTile + (tid & ~63)) * 4));
+    }
+    __device__ __forceinline__ void fetch_stage_routes(int at) {  // at: the stage's number
+        if (!G::WEIGHTS || at >= total) return;
+        if (threadIdx.x < kWave)
+            dma4(p.route + routes.t.first + min(routes.s * kHgK + (int)threadIdx.x, routes.t.red - 1),
+                 __builtin_amdgcn_readfirstlane(l.route_at + (at & (kHgRing - 1)) * kHgK * 4));
+        step(routes);
+    }
+    // before the copies of stage `at`
+    __device__ __forceinline__ void open(int at) {
+        if (ahead.s == 0) {
+            hg_open<G>(p, ahead.t, ahead.k, l, c);
+            if (G::SWIGLU && p.probs) {
+                const int tid = threadIdx.x;
+                const int v = l.route[(ahead.k & 1) * kHgTile + min(tid, ahead.t.rows - 1)];
+                dma4(p.probs + hg_route(p, v),
+                     __builtin_amdgcn_readfirstlane(l.weight_at + (ahead.k % 3 * kHgTile + (tid & ~63)) * 4));
+            }
+            fetch_tile_routes(ahead.k + 1);
+        }
+        if constexpr (G::WEIGHTS) {
+            hg_stage_rows<G>(p, c, l, ahead.s, at & (kHgRing - 1), p.gather == 1, 2 * p.M, c.ca, c.va);
+            hg_stage_rows<G>(p, c, l, ahead.s, at & (kHgRing - 1), p.gather == 2, 2 * p.N, c.cb, c.vb);
+        }
+    }
+
+    // Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS, copies two stages ahead,
+    // and rounds and stores the sums.
+    template <int NP>
+    __device__ __forceinline__ void multiply_tile(const HgTile &t, int k);
+};
+
+template <typename G>
+template <int NP>
+__device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) {
+    constexpr int T = G::T, J = G::J;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ns = (t.red + kHgK - 1) / kHgK;
+
+    v16f acc[NP][2] = {};
+    v4i w[2][4], a[2][4];  // columns of the stage, rows of the two fragments that are multiplied
+    // Two row fragments by two column fragments: four sums that take turns, so that no product
+    // waits for the one before it.  between(k) comes after the k-th of its 16 products: reads and copies
+    // there, one or two at a time, as a batch of either holds the products up while it is taken in.
+    auto multiply = [&](int pair, auto between) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v16f &d = acc[2 * pair + i][j];
+                    d = hg_mfma<T>(w[j][h], a[i][h], d);
+                    __builtin_amdgcn_sched_barrier(0);
+                    between(4 * h + 2 * i + j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        // the sums are wanted here: without this the compiler puts a stage's products together
+        // behind its barrier and copies, where the reads no longer overlap them
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[2 * pair + i][j]));
+    };
+    auto slot_at = [&](int g) { return l.data + (g & 1) * 2 * kHgOperand; };
+    // two fragments of rows or columns in eight steps, in the order in which products want them
+    auto read_a = [&](int k8, int f, v4i(&v)[2][4]) { ra.read(f + (k8 & 1), k8 >> 1, v[k8 & 1][k8 >> 1]); };
+    auto read_b = [&](int k8, v4i(&v)[2][4]) { rb.read(2 * wave + (k8 & 1), k8 >> 1, v[k8 & 1][k8 >> 1]); };
+
+    if (ns > 0) {
+        ra.at = slot_at(stage);
+        rb.at = slot_at(stage) + kHgOperand;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            read_b(i, w);
+            read_a(i, 0, a);
+        }
+    }
+    // Waits for the next stage: for all but the newest NEWER of the wave's copies, and in the first stage,
+    // whose copies are older than the last tile's stores, not for those either.
+    auto wait_copies = [&](int s, auto newer) {
+        constexpr int NEWER = newer.value, U = 4 * J;
+        if (s > 0 || stores == 0) wait_vmcnt<NEWER>();
+        else if (stores == 1) wait_vmcnt<NEWER + U>();
+        else if (stores == 2) wait_vmcnt<NEWER + 2 * U>();
+        else wait_vmcnt<NEWER + 3 * U>();
+    };
+    typedef std::integral_constant<int, 0> None;
+    typedef std::integral_constant<int, 8> Columns;
+    auto one_stage = [&](int s, auto copies) {
+        ra.at = slot_at(stage);
+        // the stage's columns are in registers, and their place is free
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if constexpr (copies.value) open(stage + 2);
+        const HgIssue<G> issue_b(p, c, l, true, ahead.s, stage & 1), issue_a(p, c, l, false, ahead.s, stage & 1);
+        if constexpr (copies.value)
+            if (NP == 2) hg_all(issue_b);
+        v4i na[2][4] = {}, nw[2][4] = {};
+        auto shift = [&]() {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) a[i][h] = na[i][h];
+        };
+#pragma unroll
+        for (int pair = 0; pair + 1 < NP / 2; ++pair) {
+            multiply(pair, [&](int i) {
+                if (i < 8) read_a(i, 2 * (pair + 1), na);
+                if constexpr (copies.value)
+                    if (pair == 0 && i < 8) issue_b.copy(i);
+            });
+            shift();
+        }
+        if (copies.value || stage + 1 < total) {
+            if constexpr (copies.value) wait_copies(s, Columns{});
+            else wait_copies(s, None{});
+            __syncthreads();
+        }
+        ra.at = slot_at(stage + 1);
+        rb.at = slot_at(stage + 1) + kHgOperand;
+        multiply(NP / 2 - 1, [&](int i) {
+            if (i < 8) {
+                read_b(i, nw);
+                read_a(i, 0, na);
+            }
+            if constexpr (copies.value)
+                if (i >= 8) issue_a.copy(i - 8);
+        });
+        if constexpr (copies.value) {
+            step(ahead);
+            fetch_stage_routes(stage + 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) w[j][h] = nw[j][h];
+        shift();
+        ++stage;
+    };
+    const int with_copies = min(ns, max(0, total - 2 - stage));
+#pragma unroll 1
+    for (int s = 0; s < with_copies; ++s) one_stage(s, std::true_type{});
+#pragma unroll 1
+    for (int s = with_copies; s < ns; ++s) one_stage(s, std::false_type{});
+
+    // the last product's result is there after 18 wait states
+    asm volatile("s_nop 15\n\ts_nop 15");
+    const int r = lane & 31, g = lane >> 5;
+    const int n0 = t.nblk * G::COLS + wave * 32 * J;
+    const size_t out_row = G::WEIGHTS ? (size_t)t.e * p.M + t.row0 : (size_t)t.row0;
+    if (G::WEIGHTS && (p.accumulate || p.c_type == kFp32)) {
+        // four columns a lane, in fp32 or added to what is there
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            const int row = 32 * i + r;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float y[4];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) y[v] = hg_sum(acc[i][j][4 * q + v]);
+                    const int col = n0 + 32 * j + 8 * q + 4 * g;
+                    if (row >= t.rows || col >= p.N) continue;
+                    const size_t at = (out_row + row) * p.N + col;
+                    if (p.c_type == kFp32) {
+                        float4 *o = reinterpret_cast<float4 *>((float *)p.c + at);
+                        float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (p.accumulate) old = *o;
+                        *o = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
+                    } else {
+                        uint2 *o = reinterpret_cast<uint2 *>((uint16_t *)p.c + at);
+                        const uint2 old = *o;
+                        typedef Element<T> L;
+                        *o = make_uint2(L::pack(L::lo(old.x) + y[0], L::hi(old.x) + y[1]),
+                                        L::pack(L::lo(old.y) + y[2], L::hi(old.y) + y[3]));
+                    }
+                }
+        }
+        stores = 0;
+        return;
+    }
+    // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
+    // that each holds eight columns in a row and stores 16 bytes.
+    uint2 out[NP][J][4];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        __builtin_amdgcn_sched_barrier(0);  // a few sums at a time leave the accumulators
+        const float weight = G::SWIGLU && p.probs ? l.weight[k % 3 * kHgTile + 32 * i + r] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float y[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    y[v] = G::SWIGLU ? weight * hg_silu_times(hg_sum(acc[i][0][4 * q + v]), hg_sum(acc[i][1][4 * q + v]))
+                                     : hg_sum(acc[i][j][4 * q + v]);
+                out[i][j][q] = make_uint2(Element<T>::pack(y[0], y[1]), Element<T>::pack(y[2], y[3]));
+                // rounded here, not in the blocks of the stores: half the registers
+                asm volatile("" : "+v"(out[i][j][q].x), "+v"(out[i][j][q].y));
+            }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int row = 32 * i + r;
+        uint16_t *crow = (uint16_t *)p.c + (out_row + row) * p.N;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+                const auto x = __builtin_amdgcn_permlane32_swap(out[i][j][q].x, out[i][j][q + 1].x, false, false);
+                const auto y = __builtin_amdgcn_permlane32_swap(out[i][j][q].y, out[i][j][q + 1].y, false, false);
+                const int col = n0 + 32 * j + 8 * (q + g);
+                if (row < t.rows && col < p.N)
+                    *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+            }
+    }
+    // all but the last two fragments have whole rows: so many stores were made at least
+    stores = n0 + 32 * J <= p.N ? NP / 2 - 1 : 0;
+}
+
+template <typename G>
+__global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void half_gmm_kernel(HalfGmmParams p) {
+    __shared__ int s_w[4];
+    __shared__ HgSchedule s_s;
+    __shared__ HgTile s_t[kHgList];
+    __shared__ int32_t s_route[2 * kHgTile];
+    __shared__ float s_weight[G::SWIGLU ? 3 * kHgTile : 1];
+    __shared__ __align__(16) uint8_t s_data[4 * kHgOperand];
+    static_assert(kHgRing * kHgK <= 2 * kHgTile, "the ring of routes");
+
+    hg_schedule<G>(p, s_w, s_s);
+    const int total = __builtin_amdgcn_readfirstlane(s_s.total), tid = threadIdx.x;
+    // Workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share blocks of rows and
+    // columns in its L2.  Weights: a run of every round of tiles, every other one backwards, as
+    // tiles get shorter.
+    const int groups = gridDim.x >> 3, xcd = blockIdx.x & 7, in = blockIdx.x >> 3;
+    const int per = (total + 7) / 8, t0 = xcd * per + in, t1 = min(xcd * per + per, total);
+    const int v0 = xcd * groups + in, v1 = (int)gridDim.x - 1 - v0;
+    int n;
+    if (G::WEIGHTS) {
+        const int rounds = total / (int)gridDim.x, rest = total - rounds * (int)gridDim.x;
+        n = rounds + ((rounds & 1 ? v1 : v0) < rest);
+    } else {
+        n = t0 < t1 ? (t1 - t0 + groups - 1) / groups : 0;
+    }
+    if (n == 0) return;
+    auto look_up = [&](int k) {  // half of the list, from tile k on
+        if (tid < kHgList / 2 && k + tid < n) {
+            const int i = k + tid;
+            s_t[i & (kHgList - 1)] =
+                hg_find_tile<G>(p, s_s, G::WEIGHTS ? i * (int)gridDim.x + (i & 1 ? v1 : v0) : t0 + i * groups);
+        }
+    };
+    look_up(0);
+    look_up(kHgList / 2);
+    int stages = n * (p.K / kHgK);
+    if constexpr (G::WEIGHTS) {  // tiles of experts without rows, the last ones, have none
+        if (tid < 4) s_w[tid] = 0;
+        __syncthreads();
+        int mine = 0;
+        for (int i = tid; i < n; i += kHgThreads)
+            mine += (hg_find_tile<G>(p, s_s, i * (int)gridDim.x + (i & 1 ? v1 : v0)).red + kHgK - 1) / kHgK;
+        atomicAdd(&s_w[0], mine);  // of integers: in any order
+        __syncthreads();
+        stages = __builtin_amdgcn_readfirstlane(s_w[0]);
+    }
+    __syncthreads();
+
+    const HgLds l{s_data, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)), s_route, s_weight,
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_route)),
+                  (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_weight))};
+    HgRun<G> run{p, l, s_t, n};
+    run.ra.lane_places();
+    run.rb.lane_places();
+    run.stage = run.stores = 0;
+    run.total = stages;
+    run.ahead.k = run.routes.k = 0;
+    run.seek(run.ahead);
+    run.seek(run.routes);
+    // the first routes, then the first two stages
+    run.fetch_tile_routes(0);
+    for (int i = 0; i < 4; ++i) run.fetch_stage_routes(i);
+    wait_vmcnt<0>();
+    __syncthreads();
+    for (int i = 0; i < min(2, stages); ++i) {
+        run.open(i);
+        hg_all(HgIssue<G>(p, run.c, l, true, run.ahead.s, i));
+        hg_all(HgIssue<G>(p, run.c, l, false, run.ahead.s, i));
+        run.step(run.ahead);
+    }
+    if (stages > 1) wait_vmcnt<16>();
+    else wait_vmcnt<0>();
+    __syncthreads();
+    for (int k = 0; k < n; ++k) {
+        if (k > 0 && k % (kHgList / 2) == 0) {
+            __syncthreads();  // nobody looks at the older half any more: tiles without stages have no barrier
+            look_up(k + kHgList / 2);
+            __syncthreads();
+        }
+        const HgTile t = run.tile(k);
+        if constexpr (G::WEIGHTS) {
+            if (t.red == 0 && p.accumulate) continue;
+            if (t.rows > 128) run.template multiply_tile<8>(t, k);
+            else run.template multiply_tile<4>(t, k);
+        } else {
+            if (t.rows > 192) run.template multiply_tile<8>(t, k);
+            else if (t.rows > 128) run.template multiply_tile<6>(t, k);
+            else if (t.rows > 64) run.template multiply_tile<4>(t, k);
+            else run.template multiply_tile<2>(t, k);
+        }
+    }
+}
+
+// The tiles, at most.
+template <typename G>
+static long long hg_most_tiles(const HalfGmmParams &p) {
+    const long long cols = (p.N + G::COLS - 1) / G::COLS;
+    if (G::WEIGHTS) return (long long)p.E * ((p.M + kHgTile - 1) / kHgTile) * cols;
+    return ((long long)p.R / kHgTile + (p.E < p.R ? p.E : p.R)) * cols;
+}
+
+template <typename G>
+static void hg_launch(const HalfGmmParams &p, int cu_count, hipStream_t stream) {
+    const long long n = hg_most_tiles<G>(p);  // one workgroup fits a CU
+    hipLaunchKernelGGL(half_gmm_kernel<G>, dim3((unsigned)((n < cu_count ? n : cu_count) + 7) / 8 * 8), dim3(kHgThreads),
+                       0, stream, p);
+}
+
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream) {
-    const long long most = kind == kHalfWeights ? p.M : p.R;
-    const int row_blocks = (int)((most + kHalfTile - 1) / kHalfTile < 64 ? (most + kHalfTile - 1) / kHalfTile : 64);
-    const dim3 grid(row_blocks, (p.N + kHalfTile - 1) / kHalfTile, p.E);
     const bool b = type == kBf16;
-    if (kind == kHalfProduct)
-        hipLaunchKernelGGL((b ? half_gmm_kernel<kHalfProduct, kBf16> : half_gmm_kernel<kHalfProduct, kFp16>), grid, dim3(256), 0, stream, p, row_blocks);
-    else if (kind == kHalfRows)
-        hipLaunchKernelGGL((b ? half_gmm_kernel<kHalfRows, kBf16> : half_gmm_kernel<kHalfRows, kFp16>), grid, dim3(256), 0, stream, p, row_blocks);
-    else
-        hipLaunchKernelGGL((b ? half_gmm_kernel<kHalfWeights, kBf16> : half_gmm_kernel<kHalfWeights, kFp16>), grid, dim3(256), 0, stream, p, row_blocks);
+    if (kind == kHalfProduct && p.swiglu) {
+        if (b) hg_launch<HgGeom<kHalfProduct, kBf16, true>>(p, cu_count, stream);
+        else hg_launch<HgGeom<kHalfProduct, kFp16, true>>(p, cu_count, stream);
+    } else if (kind == kHalfProduct) {
+        if (b) hg_launch<HgGeom<kHalfProduct, kBf16, false>>(p, cu_count, stream);
+        else hg_launch<HgGeom<kHalfProduct, kFp16, false>>(p, cu_count, stream);
+    } else if (kind == kHalfRows) {
+        if (b) hg_launch<HgGeom<kHalfRows, kBf16, false>>(p, cu_count, stream);
+        else hg_launch<HgGeom<kHalfRows, kFp16, false>>(p, cu_count, stream);
+    } else {
+        if (b) hg_launch<HgGeom<kHalfWeights, kBf16, false>>(p, cu_count, stream);
+        else hg_launch<HgGeom<kHalfWeights, kFp16, false>>(p, cu_count, stream);
+    }
     return hipGetLastError();
 }
 
