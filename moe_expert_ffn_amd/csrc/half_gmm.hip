@@ -178,26 +178,31 @@ __device__ __forceinline__ v4i hg_buffer(const void *base, uint32_t bytes) {
                (int)__builtin_amdgcn_readfirstlane(bytes), 0x00027000};
 }
 
-// Copies of a stage: eight of each operand a wave.  A wave's pieces of an operand are 64 of its rows (along) or a
-// panel of 64 of its columns (across).
+// Where a lane's pieces of a stage come from.  A wave makes eight copies of each operand: 64 of its rows
+// (along) or a panel of 64 of its columns (across).
 template <typename G>
 struct HgCopies {
-    uint32_t va[8], vb[8];  // byte offsets of a lane's pieces (products: of the tile; weights: of a stage)
-    const uint8_t *a, *b;   // products: where they count from
-    v4i ra, rb;             // weights: the same, with bounds
-    uint32_t ca, cb;        // weights: the lane's columns
-    int first, red, e;
+    // products: byte offsets in the tile, from pointers that go on from stage to stage
+    uint32_t va[8], vb[8];
+    const uint8_t *a, *b;
+    uint32_t step_b;
+    // weights: rows past the group are out of the buffers' bounds and read as 0
+    v4i ra, rb;
+    uint32_t ca, cb;   // the lane's columns
+    int first, red, s; // the group, and the stage
+    int tok[8];        // the routes of the lane's rows
 };
 
 // column piece of a lane in its panel of columns from n0, of n that are a multiple of 128
 __device__ __forceinline__ uint32_t hg_across_column(int n0, int n) {
     const int lane = threadIdx.x & 63, c = lane & 7;
-    // halves of a panel's rows change places with bit 1 of the row, which is bit 4 of the lane: see hg_across
+    // halves of a panel's rows change places with bit 1 of the row, which is bit 4 of the lane
     int col = n0 + ((c >> 2) ^ (lane >> 4 & 1)) * 32 + (c & 3) * 8;
     if (col >= n) col = n - 64 + (col & 63);
     return 2 * (uint32_t)col;
 }
 
+// The copies of tile t, the workgroup's k-th, from its first stage on.
 template <typename G>
 __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t, int k, const HgLds &l, HgCopies<G> &c) {
     const int lane = threadIdx.x & 63;
@@ -205,9 +210,9 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
     if constexpr (G::WEIGHTS) {
         c.first = t.first;
         c.red = t.red;
+        c.s = 0;
         c.ca = hg_across_column(t.row0 + wave * 64, p.M);
         c.cb = hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
-        // of rows past the group nothing is read: their offsets are not within the buffer
         const uint32_t la = 2 * p.M, lb = 2 * p.N, tokens = p.R / p.top_k;
         c.ra = p.gather == 1 ? hg_buffer(p.a, tokens * la) : hg_buffer(p.a + (size_t)t.first * p.M, t.red * la);
         c.rb = p.gather == 2 ? hg_buffer(p.b, tokens * lb) : hg_buffer(p.b + (size_t)t.first * p.N, t.red * lb);
@@ -230,41 +235,48 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
         }
         c.a = uniform_ptr((const uint8_t *)p.a);
         c.b = uniform_ptr((const uint8_t *)(p.b + (size_t)t.e * G::F * p.N * p.K));
+        c.step_b = G::B_ACROSS ? kHgK * 2 * p.N : kHgK * 2;
     }
 }
 
-// weights: offsets of the pieces of stage s, one operand
+// weights: the i-th copy's byte offset
 template <typename G>
-__device__ __forceinline__ void hg_stage_rows(const HalfGmmParams &p, const HgCopies<G> &c, const HgLds &l, int s, int ring,
-                                              bool gathered, uint32_t ld, uint32_t col, uint32_t (&v)[8]) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 8 * i + (lane >> 3), d = s * kHgK + r;
-        const uint32_t row = gathered ? hg_token(p, l.route[ring * kHgK + r]) : (uint32_t)d;
-        v[i] = d < c.red ? row * ld + col : 0xffffff00u;  // an array has at most so many bytes
-    }
+__device__ __forceinline__ uint32_t hg_offset(const HalfGmmParams &p, const HgCopies<G> &c, int i, bool gathered,
+                                              uint32_t ld, uint32_t col) {
+    const int d = c.s * kHgK + 8 * i + (int)((threadIdx.x & 63) >> 3);
+    const uint32_t row = gathered ? hg_token(p, c.tok[i]) : (uint32_t)d;
+    return d < c.red ? row * ld + col : 0xffffff00u;  // an array has at most so many bytes
 }
 
 template <typename G>
-struct HgIssue {  // the copies of one operand's stage s into slot `slot`
+struct HgIssue {  // the copies of one operand's stage into slot `slot`
+    const HalfGmmParams &p;
     const HgCopies<G> &c;
-    const uint32_t (&v)[8];
     const uint8_t *base;
     v4i rsrc;
     uint32_t at;
-    bool nt;
-    __device__ __forceinline__ HgIssue(const HalfGmmParams &p, const HgCopies<G> &c_, const HgLds &l, bool b, int s, int slot)
-        : c(c_), v(b ? c_.vb : c_.va), nt(b) {
-        at = l.data_at + (2 * slot + b) * kHgOperand + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 8192;
-        if constexpr (G::WEIGHTS) rsrc = b ? c.rb : c.ra;
-        else if (!b || !G::B_ACROSS) base = uniform_ptr((b ? c.b : c.a) + s * 128);
-        else base = uniform_ptr(c.b + (size_t)s * kHgK * (2 * p.N));
+    bool b;
+    __device__ __forceinline__ HgIssue(const HalfGmmParams &p_, const HgCopies<G> &c_, const HgLds &l, bool b_, int slot)
+        : p(p_), c(c_), b(b_) {
+        at = __builtin_amdgcn_readfirstlane(l.data_at + (2 * slot + b) * kHgOperand + (threadIdx.x >> 6) * 8192);
+        if constexpr (G::WEIGHTS) {
+            const v4i r = b ? c.rb : c.ra;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rsrc[i] = __builtin_amdgcn_readfirstlane(r[i]);
+        } else {
+            base = uniform_ptr(b ? c.b : c.a);
+        }
     }
     __device__ __forceinline__ void copy(int i) const {
-        if constexpr (G::WEIGHTS) dma16_buffer(rsrc, v[i], at + i * 1024);
-        else if (nt) dma16_nt(base, v[i], at + i * 1024);
-        else dma16(base, v[i], at + i * 1024);
+        if constexpr (G::WEIGHTS) {
+            const uint32_t v = b ? hg_offset<G>(p, c, i, p.gather == 2, 2 * p.N, c.cb)
+                                 : hg_offset<G>(p, c, i, p.gather == 1, 2 * p.M, c.ca);
+            dma16_buffer(rsrc, v, at + i * 1024);
+        } else if (b) {
+            dma16_nt(base, c.vb[i], at + i * 1024);
+        } else {
+            dma16(base, c.va[i], at + i * 1024);
+        }
     }
 };
 template <typename I>
@@ -321,38 +333,22 @@ __device__ __forceinline__ float hg_silu_times(float u, float g) {
     return u * __builtin_amdgcn_rcpf(d) * g;
 }
 
-// Where the copies are: stage s of the workgroup's tile k.
-struct HgCursor {
-    int k, s, ns;
-    HgTile t;
-};
-
 template <typename G>
 struct HgRun {
     const HalfGmmParams &p;
     const HgLds &l;
     const HgTile *list;
-    int n;              // tiles of this workgroup
-    HgCursor ahead;     // the next stage to copy
-    HgCursor routes;    // weights: the next stage whose routes are copied
+    int n;             // tiles of this workgroup
+    int stage, total;  // of all of the workgroup's: the one that is multiplied next, and how many there are
     HgCopies<G> c;
-    int stage, total;   // of all of the workgroup's: the one that is multiplied next, and how many there are
-    int stores;         // at least 4 J times as many stores have been made since the last copies
+    int tile_k, left;  // the tile whose stages are copied, and how many of them are left
+    int route_k, route_s, route_left;  // weights: the next stage whose routes are copied
     HgRead<G::A_ACROSS> ra;
     HgRead<G::B_ACROSS> rb;
 
     __device__ __forceinline__ HgTile tile(int k) const { return hg_uniform(list[k & (kHgList - 1)]); }
-    __device__ __forceinline__ void seek(HgCursor &x) const {  // the first stage of tile x.k
-        x.s = 0;
-        x.t = tile(x.k);  // past the last tile what the list happens to hold, which nobody copies
-        x.ns = (x.t.red + kHgK - 1) / kHgK;
-    }
-    __device__ __forceinline__ void step(HgCursor &x) const {
-        if (++x.s < x.ns) return;
-        ++x.k;
-        seek(x);
-    }
-    // products: the routes of tile k's rows; weights: those of a stage
+    __device__ __forceinline__ static int stages(const HgTile &t) { return (t.red + kHgK - 1) / kHgK; }
+    // products: the routes of tile k's rows; weights: those of the workgroup's stage `at`, of 64 rows
     __device__ __forceinline__ void fetch_tile_routes(int k) const {
         if (G::WEIGHTS || !p.route || k >= n) return;
         const HgTile t = tile(k);
@@ -360,29 +356,49 @@ struct HgRun {
         dma4(p.route + t.row0 + min(tid, t.rows - 1),
              __builtin_amdgcn_readfirstlane(l.route_at + ((k & 1) * kHgTile + (tid & ~63)) * 4));
     }
-    __device__ __forceinline__ void fetch_stage_routes(int at) {  // at: the stage's number
+    __device__ __forceinline__ void fetch_stage_routes(int at) {
         if (!G::WEIGHTS || at >= total) return;
-        if (threadIdx.x < kWave)
-            dma4(p.route + routes.t.first + min(routes.s * kHgK + (int)threadIdx.x, routes.t.red - 1),
+        if (route_left == 0) {
+            ++route_k;
+            route_s = 0;
+            route_left = stages(tile(route_k));  // not 0: tiles without stages come last
+        }
+        if (threadIdx.x < kWave) {
+            const HgTile t = tile(route_k);
+            dma4(p.route + t.first + min(route_s * kHgK + (int)threadIdx.x, t.red - 1),
                  __builtin_amdgcn_readfirstlane(l.route_at + (at & (kHgRing - 1)) * kHgK * 4));
-        step(routes);
+        }
+        ++route_s;
+        --route_left;
     }
-    // before the copies of stage `at`
-    __device__ __forceinline__ void open(int at) {
-        if (ahead.s == 0) {
-            hg_open<G>(p, ahead.t, ahead.k, l, c);
-            if (G::SWIGLU && p.probs) {
-                const int tid = threadIdx.x;
-                const int v = l.route[(ahead.k & 1) * kHgTile + min(tid, ahead.t.rows - 1)];
-                dma4(p.probs + hg_route(p, v),
-                     __builtin_amdgcn_readfirstlane(l.weight_at + (ahead.k % 3 * kHgTile + (tid & ~63)) * 4));
-            }
-            fetch_tile_routes(ahead.k + 1);
+    // before the copies of a stage, and behind them
+    __device__ __forceinline__ void open() {
+        if (left > 0) return;
+        ++tile_k;
+        const HgTile t = tile(tile_k);
+        left = stages(t);
+        hg_open<G>(p, t, tile_k, l, c);
+        if (G::SWIGLU && p.probs) {
+            const int tid = threadIdx.x;
+            const int v = l.route[(tile_k & 1) * kHgTile + min(tid, t.rows - 1)];
+            dma4(p.probs + hg_route(p, v),
+                 __builtin_amdgcn_readfirstlane(l.weight_at + (tile_k % 3 * kHgTile + (tid & ~63)) * 4));
         }
+        fetch_tile_routes(tile_k + 1);
+    }
+    __device__ __forceinline__ void close() {
+        --left;
         if constexpr (G::WEIGHTS) {
-            hg_stage_rows<G>(p, c, l, ahead.s, at & (kHgRing - 1), p.gather == 1, 2 * p.M, c.ca, c.va);
-            hg_stage_rows<G>(p, c, l, ahead.s, at & (kHgRing - 1), p.gather == 2, 2 * p.N, c.cb, c.vb);
+            ++c.s;
+        } else {
+            c.a += kHgK * 2;
+            c.b += c.step_b;
         }
+    }
+    // weights: the route of the lane's rows of the i-th copies of stage `at`
+    __device__ __forceinline__ void read_route(int at, int i) {
+        if constexpr (G::WEIGHTS)
+            c.tok[i] = l.route[(at & (kHgRing - 1)) * kHgK + 8 * i + (int)((threadIdx.x & 63) >> 3)];
     }
 
     // Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS, copies two stages ahead,
@@ -438,23 +454,16 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
             read_a(i, 0, a);
         }
     }
-    // Waits for the next stage: for all but the newest NEWER of the wave's copies, and in the first stage,
-    // whose copies are older than the last tile's stores, not for those either.
-    auto wait_copies = [&](int s, auto newer) {
-        constexpr int NEWER = newer.value, U = 4 * J;
-        if (s > 0 || stores == 0) wait_vmcnt<NEWER>();
-        else if (stores == 1) wait_vmcnt<NEWER + U>();
-        else if (stores == 2) wait_vmcnt<NEWER + 2 * U>();
-        else wait_vmcnt<NEWER + 3 * U>();
-    };
-    typedef std::integral_constant<int, 0> None;
-    typedef std::integral_constant<int, 8> Columns;
+    // The copies are spread over a stage, as four waves make them at once and a copy takes longer to be taken in
+    // than a product: those of the columns over the products before the barrier, those of the rows over the
+    // rest.  (In eight slots in a row each: 5% slower.)
+    constexpr int FROM = G::WEIGHTS ? 8 : 1, EVERY = NP == 8 ? (G::WEIGHTS ? 5 : 6) : NP == 6 ? 4 : G::WEIGHTS ? 1 : 2;
     auto one_stage = [&](int s, auto copies) {
         ra.at = slot_at(stage);
         // the stage's columns are in registers, and their place is free
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if constexpr (copies.value) open(stage + 2);
-        const HgIssue<G> issue_b(p, c, l, true, ahead.s, stage & 1), issue_a(p, c, l, false, ahead.s, stage & 1);
+        if constexpr (copies.value) open();
+        const HgIssue<G> issue_b(p, c, l, true, stage & 1), issue_a(p, c, l, false, stage & 1);
         if constexpr (copies.value)
             if (NP == 2) hg_all(issue_b);
         v4i na[2][4] = {}, nw[2][4] = {};
@@ -467,29 +476,30 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
 #pragma unroll
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
             multiply(pair, [&](int i) {
-                if (i < 8) read_a(i, 2 * (pair + 1), na);
-                if constexpr (copies.value)
-                    if (pair == 0 && i < 8) issue_b.copy(i);
+                if ((i & 1) == 0) read_a(i / 2, 2 * (pair + 1), na);
+                if constexpr (copies.value) {
+                    if (pair == 0 && i < 8) read_route(stage + 2, i);
+                    const int at = 16 * pair + i - FROM;
+                    if (at >= 0 && at % EVERY == 0 && at / EVERY < 8) issue_b.copy(at / EVERY);
+                }
             });
             shift();
         }
         if (copies.value || stage + 1 < total) {
-            if constexpr (copies.value) wait_copies(s, Columns{});
-            else wait_copies(s, None{});
+            // all but the columns of the stage after the next
+            wait_vmcnt<copies.value ? 8 : 0>();
             __syncthreads();
         }
         ra.at = slot_at(stage + 1);
         rb.at = slot_at(stage + 1) + kHgOperand;
         multiply(NP / 2 - 1, [&](int i) {
-            if (i < 8) {
-                read_b(i, nw);
-                read_a(i, 0, na);
-            }
+            if (i & 1) read_a(i / 2, 0, na);
+            else read_b(i / 2, nw);
             if constexpr (copies.value)
-                if (i >= 8) issue_a.copy(i - 8);
+                if (i & 1) issue_a.copy(i / 2);
         });
         if constexpr (copies.value) {
-            step(ahead);
+            close();
             fetch_stage_routes(stage + 4);
         }
 #pragma unroll
@@ -540,7 +550,6 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
                     }
                 }
         }
-        stores = 0;
         return;
     }
     // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
@@ -580,8 +589,6 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
                     *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
             }
     }
-    // all but the last two fragments have whole rows: so many stores were made at least
-    stores = n0 + 32 * J <= p.N ? NP / 2 - 1 : 0;
 }
 
 template <typename G>
@@ -638,21 +645,22 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     HgRun<G> run{p, l, s_t, n};
     run.ra.lane_places();
     run.rb.lane_places();
-    run.stage = run.stores = 0;
+    run.stage = 0;
     run.total = stages;
-    run.ahead.k = run.routes.k = 0;
-    run.seek(run.ahead);
-    run.seek(run.routes);
+    run.tile_k = run.route_k = -1;
+    run.left = run.route_left = 0;
     // the first routes, then the first two stages
     run.fetch_tile_routes(0);
     for (int i = 0; i < 4; ++i) run.fetch_stage_routes(i);
     wait_vmcnt<0>();
     __syncthreads();
     for (int i = 0; i < min(2, stages); ++i) {
-        run.open(i);
-        hg_all(HgIssue<G>(p, run.c, l, true, run.ahead.s, i));
-        hg_all(HgIssue<G>(p, run.c, l, false, run.ahead.s, i));
-        run.step(run.ahead);
+        run.open();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) run.read_route(i, j);
+        hg_all(HgIssue<G>(p, run.c, l, true, i));
+        hg_all(HgIssue<G>(p, run.c, l, false, i));
+        run.close();
     }
     if (stages > 1) wait_vmcnt<16>();
     else wait_vmcnt<0>();
