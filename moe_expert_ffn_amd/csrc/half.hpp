@@ -20,6 +20,9 @@ struct HalfGmmParams {
     int swiglu, accumulate;
     int c_type;              // kFp32 in kHalfWeights alone
 };
+// ... of few rows an expert (half_few.hip)
+bool half_few_ok(const HalfGmmParams &p);
+hipError_t launch_half_few(const HalfGmmParams &p, int type, hipStream_t stream);
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream);
 
 // SwiGLU of 16-bit rows and its gradient (half_swiglu.hip).

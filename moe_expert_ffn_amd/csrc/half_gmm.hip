@@ -11,27 +11,12 @@
 
 #include "common.hpp"
 #include "dma.hpp"
-#include "element.hpp"
-#include "half.hpp"
+#include "half_gmm.hpp"
 
 namespace megamoe {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ int hg_row_end(const HalfGmmParams &p, int e) {
-    const int v = e >= 0 ? p.cumsum[e] : 0;
-    return v < 0 ? 0 : v > p.R ? p.R : v;
-}
-
-// The token of a sorted route: what lies past the valid rows stays in bounds.
-__device__ __forceinline__ uint32_t hg_route(const HalfGmmParams &p, int v) { return v < 0 ? 0 : v < p.R ? v : p.R - 1; }
-__device__ __forceinline__ uint32_t hg_token(const HalfGmmParams &p, int v) {
-    const uint32_t u = hg_route(p, v);
-    return p.top_k == 1 ? u : __umulhi(u, p.top_k_inv);
-}
 
 // 32 x 32 x 16 with the columns' operand first: lane l holds output row l & 31 and the columns
 // 8 q + 4 (l >> 5) + 0..3, q = 0..3.  Of either operand lane l has row l & 31 and 8 (l >> 5) + 0..7 of the reduction.
@@ -63,7 +48,6 @@ __device__ __forceinline__ v16f hg_mfma(v4i w, v4i a, v16f acc) {
 // The grid is persistent, and the copies run two stages ahead of the products through the workgroup's
 // tiles, so that a tile's first stages are there when the tile before has been rounded and stored.
 constexpr int kHgThreads = 256;
-constexpr int kHgE = 256;
 constexpr int kHgTile = 256, kHgK = 64;
 constexpr int kHgOperand = kHgTile * kHgK * 2;  // bytes of an operand's stage
 constexpr int kHgList = 64;                     // tiles looked up ahead, half of them at a time
@@ -139,10 +123,14 @@ __device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgS
             else lo = mid + 1;
         }
         const int rows = s.rows[lo], local = t - s.pre[lo];
-        const int mb = (rows + kHgTile - 1) / kHgTile, m = local % mb;
+        // eight row blocks, then the columns, then the next eight: what an XCD's workgroups multiply at one time
+        // shares most (16 row blocks, us: row gradient 1668 -> 1594, product 1602 -> 1590)
+        const int mb = (rows + kHgTile - 1) / kHgTile, nb = (p.N + G::COLS - 1) / G::COLS;
+        const int run = local / (8 * nb), wide = min(8, mb - 8 * run), in = local - 8 * nb * run;
+        const int m = 8 * run + in % wide;
         const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
         const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
-        return HgTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, local / mb, 0, p.K};
+        return HgTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, in / wide, 0, p.K};
     }
 }
 __device__ __forceinline__ HgTile hg_uniform(const HgTile &x) {
@@ -325,12 +313,6 @@ __device__ __forceinline__ float hg_sum(float a) {
     float v;
     asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
     return v;
-}
-
-// silu(u) * g for a result that is rounded to 16 bits: the reciprocal's last ulp is not corrected
-__device__ __forceinline__ float hg_silu_times(float u, float g) {
-    const float d = __builtin_amdgcn_exp2f(u * -1.4426950408889634f) + 1.0f;
-    return u * __builtin_amdgcn_rcpf(d) * g;
 }
 
 template <typename G>
@@ -702,6 +684,7 @@ static void hg_launch(const HalfGmmParams &p, int cu_count, hipStream_t stream) 
 
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream) {
     const bool b = type == kBf16;
+    if (kind == kHalfProduct && half_few_ok(p)) return launch_half_few(p, type, stream);
     if (kind == kHalfProduct && p.swiglu) {
         if (b) hg_launch<HgGeom<kHalfProduct, kBf16, true>>(p, cu_count, stream);
         else hg_launch<HgGeom<kHalfProduct, kFp16, true>>(p, cu_count, stream);
