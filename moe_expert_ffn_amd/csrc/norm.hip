@@ -85,8 +85,8 @@ __device__ __forceinline__ void norm_gate(const NormParams &p, size_t t, int col
 }
 
 // A token a workgroup; a thread has the C columns of 8 that lie blockDim.x * 8 apart.
-template <int TX, int TB, int C>
-__global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
+template <int TX, int TB, int C, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_kernel(NormParams p) {
     __shared__ float s_a[16], s_b[16];
     const size_t t = blockIdx.x;
     const int waves = blockDim.x >> 6;
@@ -155,99 +155,122 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormParams p) {
 }
 
 // Backwards.  A workgroup goes on to further tokens and keeps its sums over them for every column; they
-// go to the workspace, and a second kernel adds them up in a fixed order.
-template <int TX, int TB, int C>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(NormParams p) {
+// go to the workspace, and a second kernel adds them up in a fixed order.  What it waits for is memory: a token's
+// rows are asked for together, and kept as they are stored until both of the token's reductions are done.
+template <int TX, int TB, int C, int THREADS>
+__global__ __launch_bounds__(THREADS, C == 1 ? 4 : 2) void norm_grad_kernel(NormParams p) {
     __shared__ float s_a[2][48], s_b[2][32];
     const int waves = blockDim.x >> 6;
     const float inv_k = 1.0f / (float)p.K;
-    const bool block = p.s != nullptr;
+    const bool block = p.s != nullptr, before = p.w_before != nullptr, after = p.w_after != nullptr;
     float wb_sum[C][8] = {}, wa_sum[C][8] = {}, gate_sum[C][8] = {}, one_sum = 0.0f;
     int flip = 0;
     for (size_t t = blockIdx.x; t < (size_t)p.M; t += gridDim.x, flip ^= 1) {
-        float r[C][8], s[C][8], dh[C][8], sum[3] = {0.0f, 0.0f, 0.0f};
+        typename Element<TX>::Raw r_raw[C], dr_raw[C];
+        typename Element<TB>::Raw s_raw[C];
+        float dh[C][8], sum[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int col = (threadIdx.x + i * blockDim.x) * 8;
             if (col >= p.K) continue;
-            if (p.w_before) {
+            if (before) r_raw[i] = Element<TX>::load_nt(p.r, t * p.K + col);
+            if (p.dr) dr_raw[i] = Element<TX>::load_nt(p.dr, t * p.K + col);
+            if (block) s_raw[i] = Element<TB>::load_nt(p.s, t * p.K + col);
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = (threadIdx.x + i * blockDim.x) * 8;
+            if (col >= p.K) continue;
+            float v[8];
+            if (before) {
                 float w[8];
-                Element<TX>::values(Element<TX>::load(p.r, t * p.K + col), r[i]);
                 if (p.h_type == kFp32) norm_rows<kFp32>(p.h, p.row_of, t, p.top_k, p.R, p.K, col, dh[i]);
                 else if (p.h_type == kFp16) norm_rows<kFp16>(p.h, p.row_of, t, p.top_k, p.R, p.K, col, dh[i]);
                 else norm_rows<kBf16>(p.h, p.row_of, t, p.top_k, p.R, p.K, col, dh[i]);
                 Element<kFp32>::values(Element<kFp32>::load(p.w_before, col), w);
+                Element<TX>::values(r_raw[i], v);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    sum[0] += r[i][j] * r[i][j];
-                    sum[1] += dh[i][j] * w[j] * r[i][j];
+                    sum[0] += v[j] * v[j];
+                    sum[1] += dh[i][j] * w[j] * v[j];
                 }
             }
             if (block) {
-                Element<TB>::values(Element<TB>::load(p.s, t * p.K + col), s[i]);
+                Element<TB>::values(s_raw[i], v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[2] += s[i][j] * s[i][j];
+                for (int j = 0; j < 8; ++j) sum[2] += v[j] * v[j];
             }
         }
         norm_sum(sum, s_a[flip], waves);
         const float rstd_r = 1.0f / sqrtf(sum[0] * inv_k + p.eps);
-        const float rstd_s = p.w_after ? 1.0f / sqrtf(sum[2] * inv_k + p.eps) : 1.0f;
+        const float rstd_s = after ? 1.0f / sqrtf(sum[2] * inv_k + p.eps) : 1.0f;
         const float mean_r = sum[1] * inv_k * rstd_r * rstd_r;
         float dot[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int col = (threadIdx.x + i * blockDim.x) * 8;
             if (col >= p.K) continue;
-            float g[8];
-            if (p.dr) Element<TX>::values(Element<TX>::load(p.dr, t * p.K + col), g);
+            float g[8], v[8], w[8];
+            if (p.dr) Element<TX>::values(dr_raw[i], g);
             else
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g[j] = 0.0f;
-            if (p.w_before) {
-                float w[8];
+            if (before) {
+                Element<TX>::values(r_raw[i], v);
                 Element<kFp32>::values(Element<kFp32>::load(p.w_before, col), w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    wb_sum[i][j] += dh[i][j] * (r[i][j] * rstd_r);
-                    g[j] += rstd_r * (dh[i][j] * w[j] - r[i][j] * mean_r);
+                    wb_sum[i][j] += dh[i][j] * (v[j] * rstd_r);
+                    g[j] += rstd_r * (dh[i][j] * w[j] - v[j] * mean_r);
                 }
             }
-            Element<TX>::store(p.dx, t * p.K + col, g);
+            Element<TX>::store_nt(p.dx, t * p.K + col, g);
             if (!block) continue;
-            float gate[8], w[8], n[8];
+            Element<TB>::values(s_raw[i], v);
+            if (after) Element<kFp32>::values(Element<kFp32>::load(p.w_after, col), w);
+            if (p.dgate) {  // the gate's own gradient
+                float n[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    n[j] = p.alpha * g[j] * (v[j] * rstd_s * (after ? w[j] : 1.0f));
+                    dot[1] += n[j];
+                }
+                if (p.gate_cols != 1) {
+                    if (p.gate_rows == 1)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) gate_sum[i][j] += n[j];
+                    else store_values(p.dgate, p.gate_type, t * p.K + col, n);
+                }
+            }
+            float gate[8];
             norm_gate(p, t, col, gate);
-            if (p.w_after) Element<kFp32>::values(Element<kFp32>::load(p.w_after, col), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float sh = s[i][j] * rstd_s, wj = p.w_after ? w[j] : 1.0f;
-                n[j] = p.alpha * g[j] * (sh * wj);  // the gate's gradient
                 g[j] *= gate[j];
-                if (p.w_after) wa_sum[i][j] += g[j] * sh;
-                g[j] *= wj;
-                dot[0] += g[j] * s[i][j];
-                dot[1] += n[j];
+                if (after) {
+                    wa_sum[i][j] += g[j] * (v[j] * rstd_s);
+                    g[j] *= w[j];
+                    dot[0] += g[j] * v[j];
+                }
                 dh[i][j] = g[j];
             }
-            if (!p.dgate || p.gate_cols == 1) continue;
-            if (p.gate_rows == 1)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) gate_sum[i][j] += n[j];
-            else store_values(p.dgate, p.gate_type, t * p.K + col, n);
         }
         if (!block) continue;
-        norm_sum(dot, s_b[flip], waves);
+        if (after || (p.dgate && p.gate_cols == 1)) norm_sum(dot, s_b[flip], waves);
         if (p.dgate && p.gate_cols == 1) {
             if (p.gate_rows == 1) one_sum += dot[1];
             else if (threadIdx.x == 0) store_value(p.dgate, p.gate_type, t, dot[1]);
         }
-        const float mean_s = p.w_after ? dot[0] * inv_k * rstd_s * rstd_s : 0.0f;
+        const float mean_s = after ? dot[0] * inv_k * rstd_s * rstd_s : 0.0f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int col = (threadIdx.x + i * blockDim.x) * 8;
             if (col >= p.K) continue;
+            float v[8];
+            Element<TB>::values(s_raw[i], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dh[i][j] = rstd_s * (dh[i][j] - s[i][j] * mean_s);
-            Element<TB>::store(p.ds, t * p.K + col, dh[i]);
+            for (int j = 0; j < 8; ++j) dh[i][j] = rstd_s * (dh[i][j] - v[j] * mean_s);
+            Element<TB>::store_nt(p.ds, t * p.K + col, dh[i]);
         }
     }
     const size_t n = gridDim.x;
@@ -256,52 +279,56 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(NormParams p) {
         const int col = (threadIdx.x + i * blockDim.x) * 8;
         if (col >= p.K) continue;
         const size_t at = blockIdx.x * (size_t)p.K + col;
-        if (p.w_before) Element<kFp32>::store(p.part, at, wb_sum[i]);
-        if (p.w_after) Element<kFp32>::store(p.part, n * p.K + at, wa_sum[i]);
+        if (before) Element<kFp32>::store(p.part, at, wb_sum[i]);
+        if (after) Element<kFp32>::store(p.part, n * p.K + at, wa_sum[i]);
         if (p.dgate && p.gate_rows == 1 && p.gate_cols != 1) Element<kFp32>::store(p.part, 2 * n * p.K + at, gate_sum[i]);
     }
     if (p.dgate && p.gate_rows == 1 && p.gate_cols == 1 && threadIdx.x == 0) p.part[2 * n * p.K + blockIdx.x] = one_sum;
 }
 
-// Column blockIdx.x * 64 + lane of vector blockIdx.y: the sum of its n parts, a quarter of them a wave.
-__global__ __launch_bounds__(256) void norm_columns_kernel(NormParams p, int n) {
-    __shared__ float s[4][64];
+// Column blockIdx.x * 64 + lane of vector blockIdx.y: the sum of its n parts, a sixteenth of them a wave, eight
+// asked for at a time.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(NormParams p, int n) {
+    __shared__ float s[16][64];
     const int which = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int cols = which == 2 && p.gate_cols == 1 ? 1 : p.K, col = blockIdx.x * 64 + lane;
     if (which == 0 ? !p.w_before : which == 1 ? !p.w_after : !(p.dgate && p.gate_rows == 1)) return;
     const float *part = p.part + (size_t)which * n * p.K;
     float sum = 0.0f;
     if (col < cols)
-        for (int i = wave; i < n; i += 4) sum += part[(size_t)i * cols + col];
+        for (int i = wave; i < n; i += 16 * 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = i + 16 * u < n ? part[(size_t)(i + 16 * u) * cols + col] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum += v[u];
+        }
     s[wave][lane] = sum;
     __syncthreads();
     if (wave != 0 || col >= cols) return;
-    sum = s[0][lane] + s[1][lane] + s[2][lane] + s[3][lane];
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum += s[w][lane];
     if (which == 2) store_value(p.dgate, p.gate_type, col, sum);
     else (which ? p.dw_after : p.dw_before)[col] = sum;
 }
 
-struct NormShape {
-    int threads, chunks;
-};
-static NormShape norm_shape(int K) {
-    const int n = K / 8;
-    const int c = n <= 512 ? 1 : n <= 2048 ? 2 : 4;
-    return {((n + c - 1) / c + 63) / 64 * 64, c};
-}
 int norm_grad_groups(int M) { return M < 512 ? M : 512; }
 
+template <int TX, int TB, int C, int THREADS>
+static void norm_launch_shape(const NormParams &p, bool grad, hipStream_t stream) {
+    const dim3 grid(grad ? norm_grad_groups(p.M) : p.M), block(((p.K / 8 + C - 1) / C + 63) / 64 * 64);
+    if (grad) hipLaunchKernelGGL((norm_grad_kernel<TX, TB, C, THREADS>), grid, block, 0, stream, p);
+    else hipLaunchKernelGGL((norm_kernel<TX, TB, C, THREADS>), grid, block, 0, stream, p);
+}
 template <int TX, int TB>
 static void norm_launch(const NormParams &p, bool grad, hipStream_t stream) {
-    const NormShape s = norm_shape(p.K);
-    const dim3 grid(grad ? norm_grad_groups(p.M) : p.M), block(s.threads);
-#define NORM_LAUNCH(C)                                                                          \
-    if (grad) hipLaunchKernelGGL((norm_grad_kernel<TX, TB, C>), grid, block, 0, stream, p);     \
-    else hipLaunchKernelGGL((norm_kernel<TX, TB, C>), grid, block, 0, stream, p)
-    if (s.chunks == 1) { NORM_LAUNCH(1); }
-    else if (s.chunks == 2) { NORM_LAUNCH(2); }
-    else { NORM_LAUNCH(4); }
-#undef NORM_LAUNCH
+    // up to 512 threads to a token, whose registers hold all of the gradient's values of 32 columns; past
+    // K = 16384 1024 threads, where they spill
+    if (p.K <= 4096) norm_launch_shape<TX, TB, 1, 512>(p, grad, stream);
+    else if (p.K <= 8192) norm_launch_shape<TX, TB, 2, 512>(p, grad, stream);
+    else if (p.K <= 16384) norm_launch_shape<TX, TB, 4, 512>(p, grad, stream);
+    else norm_launch_shape<TX, TB, 4, 1024>(p, grad, stream);
 }
 
 hipError_t launch_norm(const NormParams &p, int x_type, int rows_type, bool grad, hipStream_t stream) {
@@ -319,7 +346,7 @@ hipError_t launch_norm(const NormParams &p, int x_type, int rows_type, bool grad
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || !grad) return err;
     if (!p.w_before && !p.w_after && !(p.dgate && p.gate_rows == 1)) return err;
-    hipLaunchKernelGGL(norm_columns_kernel, dim3((p.K + 63) / 64, 3), dim3(256), 0, stream, p, norm_grad_groups(p.M));
+    hipLaunchKernelGGL(norm_columns_kernel, dim3((p.K + 63) / 64, 3), dim3(1024), 0, stream, p, norm_grad_groups(p.M));
     return hipGetLastError();
 }
 
