@@ -65,7 +65,8 @@ int megamoe_half_gmm2_dgrad(const megamoe_dims *d, const uint16_t *dout, int typ
  *   megamoe_half_gmm1_wgrad  dw1[e, n, k] = sum_d dc[d, n] x[t, k]
  *   megamoe_half_gmm2_wgrad  dw2[e, k, i] = sum_d dout[t, k] y[d, i]
  * dw_type: type or MEGAMOE_FP32.  accumulate nonzero: added to what dw holds (in
- * fp32, then rounded); zero: dw is written, 0 for an expert without rows. */
+ * fp32, then rounded); zero: dw is written, 0 for an expert without rows.  Their
+ * limit is (R + 64) * max(K, 2I) < 2^31 (else MEGAMOE_EUNSUPPORTED). */
 int megamoe_half_gmm1_wgrad(const megamoe_dims *d, const uint16_t *dc, const uint16_t *x, int type,
                             const int32_t *sorted_route, const int32_t *expert_cumsum, void *dw1,
                             int dw_type, int accumulate, void *stream);

@@ -15,7 +15,8 @@ struct HalfGmmParams {
     const float *probs;      // nullable, with swiglu: the weight of each route
     void *c;                 // [R, N], of kHalfWeights [E, M, N]
     int R, E, M, N, K, top_k;
-    uint32_t top_k_inv;      // ceil(2^32 / top_k), for top_k > 1
+    uint32_t top_k_inv;      // ceil(2^32 / top_k); 0 for top_k == 1, where
+    uint32_t one_k;          // this is ~0, else 0
     int gather;              // 0, 1: row d of a is row route[d] / top_k of the array, 2: of b
     int swiglu, accumulate;
     int c_type;              // kFp32 in kHalfWeights alone

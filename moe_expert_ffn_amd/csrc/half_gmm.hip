@@ -15,22 +15,24 @@
 
 namespace megamoe {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
-// 32 x 32 x 16 with the columns' operand first: lane l holds output row l & 31 and the columns
-// 8 q + 4 (l >> 5) + 0..3, q = 0..3.  Of either operand lane l has row l & 31 and 8 (l >> 5) + 0..7 of the reduction.
+// 16 x 16 x 32 with the columns' operand first: lane l holds output row l & 15 and the columns 4 (l >> 4) + 0..3.  Of
+// either operand lane l has row l & 15 and 8 (l >> 4) + 0..7 of the reduction.  (From registers, on random operands,
+// for which the card lowers its clock, it ran at 2030 TFLOP/s and the 32 x 32 x 16 form at 1730, as that one
+// goes through its sums twice as often; on zeros 2420 and 2470.)
 template <int T>
-__device__ __forceinline__ v16f hg_mfma(v4i w, v4i a, v16f acc) {
+__device__ __forceinline__ v4f hg_mfma(v4i w, v4i a, v4f acc) {
     if constexpr (T == kBf16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, a), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, a), acc, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, a), acc, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, a), acc, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
 // Tiles of 256 rows by 256 columns, four waves to a tile and one to a SIMD, each multiplying all of
-// its rows by 64 of its columns: 8 x 2 fragments of 32 x 32 sums fill half of the register file, and the time of a
+// its rows by 64 of its columns: 16 x 4 fragments of 16 x 16 sums fill half of the register file, and the time of a
 // tile follows its live rows in steps of 64.
 //
 // A stage is 64 of the reduction, copied asynchronously into one of two slots in LDS, 128 bytes (a whole
@@ -53,15 +55,16 @@ constexpr int kHgOperand = kHgTile * kHgK * 2;  // bytes of an operand's stage
 constexpr int kHgList = 64;                     // tiles looked up ahead, half of them at a time
 constexpr int kHgRing = 8;                      // stages whose routes are kept (weights' gradients)
 
-template <int KIND_, int T_, bool SWIGLU_>
+template <int KIND_, int T_, bool SWIGLU_, int GATHER_ = 0>
 struct HgGeom {
     static constexpr int KIND = KIND_, T = T_;
     static constexpr bool SWIGLU = SWIGLU_;
+    static constexpr int GATHER = GATHER_;  // weights: HalfGmmParams::gather, 1 or 2
     static constexpr bool WEIGHTS = KIND == kHalfWeights;
     static constexpr bool A_ACROSS = WEIGHTS, B_ACROSS = KIND != kHalfProduct;
     static constexpr int F = SWIGLU ? 2 : 1;
     static constexpr int COLS = kHgTile / F;  // output columns of a tile
-    static constexpr int J = 2 / F;           // fragments of 32 columns that a wave stores
+    static constexpr int J = 4 / F;           // fragments of 16 columns that a wave stores
 };
 
 struct HgTile {
@@ -176,16 +179,18 @@ struct HgCopies {
     uint32_t step_b;
     // weights: rows past the group are out of the buffers' bounds and read as 0
     v4i ra, rb;
-    uint32_t ca, cb;   // the lane's columns
-    int first, red, s; // the group, and the stage
-    int tok[8];        // the routes of the lane's rows
+    uint32_t gathered;     // byte of the lane's columns in a gathered row, in even copies
+    uint32_t straight[2];  // byte offset of the lane's first row in the other operand, in even and odd copies
+    int left;              // rows of the group from the lane's first one on
+    int tok[8];            // the routes of the lane's rows
 };
 
-// column piece of a lane in its panel of columns from n0, of n that are a multiple of 128
+// Byte of a lane's columns in its panel of columns from n0, of n that are a multiple of 128, in even copies; in odd
+// ones it is this ^ 32.  The 32-byte quarters of a panel's row change places with its bits 1 and 3: a
+// transposing load takes 32 bytes of rows 0..3, 8..11, 16..19 and 24..27, which then meet each bank twice.
 __device__ __forceinline__ uint32_t hg_across_column(int n0, int n) {
-    const int lane = threadIdx.x & 63, c = lane & 7;
-    // halves of a panel's rows change places with bit 1 of the row, which is bit 4 of the lane
-    int col = n0 + ((c >> 2) ^ (lane >> 4 & 1)) * 32 + (c & 3) * 8;
+    const int lane = threadIdx.x & 63, c = lane & 7;  // the lane's row in a copy is lane >> 3
+    int col = n0 + ((c >> 1) ^ (lane >> 4 & 1) * 2) * 16 + (c & 1) * 8;
     if (col >= n) col = n - 64 + (col & 63);
     return 2 * (uint32_t)col;
 }
@@ -196,14 +201,15 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if constexpr (G::WEIGHTS) {
-        c.first = t.first;
-        c.red = t.red;
-        c.s = 0;
-        c.ca = hg_across_column(t.row0 + wave * 64, p.M);
-        c.cb = hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
+        const uint32_t ca = hg_across_column(t.row0 + wave * 64, p.M);
+        const uint32_t cb = hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
+        c.left = t.red - (lane >> 3);
+        c.gathered = G::GATHER == 1 ? ca : cb;
+        c.straight[0] = (uint32_t)(lane >> 3) * (2 * (G::GATHER == 1 ? p.N : p.M)) + (G::GATHER == 1 ? cb : ca);
+        c.straight[1] = c.straight[0] ^ 32;
         const uint32_t la = 2 * p.M, lb = 2 * p.N, tokens = p.R / p.top_k;
-        c.ra = p.gather == 1 ? hg_buffer(p.a, tokens * la) : hg_buffer(p.a + (size_t)t.first * p.M, t.red * la);
-        c.rb = p.gather == 2 ? hg_buffer(p.b, tokens * lb) : hg_buffer(p.b + (size_t)t.first * p.N, t.red * lb);
+        c.ra = G::GATHER == 1 ? hg_buffer(p.a, tokens * la) : hg_buffer(p.a + (size_t)t.first * p.M, t.red * la);
+        c.rb = G::GATHER == 2 ? hg_buffer(p.b, tokens * lb) : hg_buffer(p.b + (size_t)t.first * p.N, t.red * lb);
     } else {
         const uint32_t la = 2 * p.K;
 #pragma unroll
@@ -213,7 +219,8 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
             const uint32_t row = p.gather ? hg_token(p, l.route[(k & 1) * kHgTile + live]) : (uint32_t)(t.row0 + live);
             c.va[i] = row * la + piece;
             if constexpr (G::B_ACROSS) {
-                c.vb[i] = (uint32_t)(8 * i + (lane >> 3)) * (2 * p.N) + hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
+                c.vb[i] = (uint32_t)(8 * i + (lane >> 3)) * (2 * p.N) +
+                          (hg_across_column(t.nblk * kHgTile + wave * 64, p.N) ^ (i & 1) * 32);
             } else {
                 // with SwiGLU a wave's columns are 32 for silu and the 32 of the gate that go with them
                 const int w = r >> 6, in = r & 63;
@@ -227,13 +234,13 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
     }
 }
 
-// weights: the i-th copy's byte offset
+// weights: the i-th copy's byte offset.  Rows past the group are not within the buffer of the straight
+// operand, whose bytes end with the group; a gathered row of theirs is put past the end.
 template <typename G>
-__device__ __forceinline__ uint32_t hg_offset(const HalfGmmParams &p, const HgCopies<G> &c, int i, bool gathered,
-                                              uint32_t ld, uint32_t col) {
-    const int d = c.s * kHgK + 8 * i + (int)((threadIdx.x & 63) >> 3);
-    const uint32_t row = gathered ? hg_token(p, c.tok[i]) : (uint32_t)d;
-    return d < c.red ? row * ld + col : 0xffffff00u;  // an array has at most so many bytes
+__device__ __forceinline__ uint32_t hg_offset(const HalfGmmParams &p, const HgCopies<G> &c, int i, int operand, uint32_t ld) {
+    if (G::GATHER != operand) return c.straight[i & 1] + (uint32_t)i * (8 * ld);
+    const uint32_t v = hg_token(p, c.tok[i]) * ld + (c.gathered ^ (i & 1) * 32);
+    return 8 * i < c.left ? v : 0xffffff00u;  // an array has at most so many bytes
 }
 
 template <typename G>
@@ -257,8 +264,7 @@ struct HgIssue {  // the copies of one operand's stage into slot `slot`
     }
     __device__ __forceinline__ void copy(int i) const {
         if constexpr (G::WEIGHTS) {
-            const uint32_t v = b ? hg_offset<G>(p, c, i, p.gather == 2, 2 * p.N, c.cb)
-                                 : hg_offset<G>(p, c, i, p.gather == 1, 2 * p.M, c.ca);
+            const uint32_t v = b ? hg_offset<G>(p, c, i, 2, 2 * p.N) : hg_offset<G>(p, c, i, 1, 2 * p.M);
             dma16_buffer(rsrc, v, at + i * 1024);
         } else if (b) {
             dma16_nt(base, c.vb[i], at + i * 1024);
@@ -277,32 +283,31 @@ __device__ __forceinline__ void hg_all(const I &issue) {
 template <bool ACROSS>
 struct HgRead {
     const uint8_t *at;
-    int place[4];  // along: of the lane's piece of each step of 16
-    int half[2];   // across: of the halves of a panel
+    int place[4];  // along: of the lane's piece of each step of 32, two; across: of the quarters of a panel
     __device__ __forceinline__ HgRead() {}
     __device__ __forceinline__ void lane_places() {
         const int lane = threadIdx.x & 63;
         if constexpr (ACROSS) {
-            // rows (lane & 15) >> 2 and 8 (lane >> 5) on, columns 16 (lane >> 4 & 1) + 4 (lane & 3) + 0..3
-            const int swap = lane >> 3 & 1;  // bit 1 of the row
-            const int in = ((lane & 15) >> 2) * 128 + (lane >> 5) * 1024 + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
-            half[0] = in + swap * 64;
-            half[1] = in + (swap ^ 1) * 64;
+            // row 8 (lane >> 4) + ((lane & 15) >> 2), and four on; columns 4 (lane & 3) + 0..3
+            const int in = (lane >> 4) * 1024 + ((lane & 15) >> 2) * 128 + (lane & 3) * 8;
+            const int swap = (lane >> 3 & 1) * 2 + (lane >> 4 & 1);  // bits 1 and 3 of the row
+#pragma unroll
+            for (int q = 0; q < 4; ++q) place[q] = in + (q ^ swap) * 32;
         } else {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) place[h] = (lane & 31) * 128 + hg_swz(lane & 31, 2 * h + (lane >> 5)) * 16;
+            for (int h = 0; h < 2; ++h) place[h] = (lane & 15) * 128 + hg_swz(lane & 15, 4 * h + (lane >> 4)) * 16;
         }
     }
-    // fragment f of 32 rows or columns, step h
+    // fragment f of 16 rows or columns, step h
     __device__ __forceinline__ void read(int f, int h, v4i &v) const {
         if constexpr (ACROSS) {
             typedef __attribute__((address_space(3))) v4s *P;
-            const uint8_t *q = at + half[f & 1] + (f >> 1) * 8192 + h * 2048;
+            const uint8_t *q = at + place[f & 3] + (f >> 2) * 8192 + h * 4096;
             const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q));
             const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 512)));
             v = v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
         } else {
-            v = *reinterpret_cast<const v4i *>(at + f * 4096 + place[h]);
+            v = *reinterpret_cast<const v4i *>(at + f * 2048 + place[h]);
         }
     }
 };
@@ -371,7 +376,10 @@ struct HgRun {
     __device__ __forceinline__ void close() {
         --left;
         if constexpr (G::WEIGHTS) {
-            ++c.s;
+            const uint32_t step = kHgK * 2 * (G::GATHER == 1 ? p.N : p.M);
+            c.straight[0] += step;
+            c.straight[1] += step;
+            c.left -= kHgK;
         } else {
             c.a += kHgK * 2;
             c.b += c.step_b;
@@ -397,35 +405,34 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ns = (t.red + kHgK - 1) / kHgK;
 
-    v16f acc[NP][2] = {};
-    v4i w[2][4], a[2][4];  // columns of the stage, rows of the two fragments that are multiplied
-    // Two row fragments by two column fragments: four sums that take turns, so that no product
-    // waits for the one before it.  between(k) comes after the k-th of its 16 products: reads and copies
-    // there, one or two at a time, as a batch of either holds the products up while it is taken in.
+    v4f acc[2 * NP][4] = {};
+    v4i w[4][2], a[4][2];  // columns of the stage, the 64 rows that are multiplied
+    // between(k) comes after every other of the 32 products: reads and copies there, one or two at a time, as a batch
+    // of either holds the products up while it is taken in.
     auto multiply = [&](int pair, auto between) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    v16f &d = acc[2 * pair + i][j];
+                for (int j = 0; j < 4; ++j) {
+                    v4f &d = acc[4 * pair + i][j];
                     d = hg_mfma<T>(w[j][h], a[i][h], d);
                     __builtin_amdgcn_sched_barrier(0);
-                    between(4 * h + 2 * i + j);
+                    if (j & 1) between(8 * h + 2 * i + (j >> 1));
                     __builtin_amdgcn_sched_barrier(0);
                 }
         // the sums are wanted here: without this the compiler puts a stage's products together
         // behind its barrier and copies, where the reads no longer overlap them
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) asm volatile("" : "+a"(acc[2 * pair + i][j]));
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[4 * pair + i][j]));
     };
     auto slot_at = [&](int g) { return l.data + (g & 1) * 2 * kHgOperand; };
-    // two fragments of rows or columns in eight steps, in the order in which products want them
-    auto read_a = [&](int k8, int f, v4i(&v)[2][4]) { ra.read(f + (k8 & 1), k8 >> 1, v[k8 & 1][k8 >> 1]); };
-    auto read_b = [&](int k8, v4i(&v)[2][4]) { rb.read(2 * wave + (k8 & 1), k8 >> 1, v[k8 & 1][k8 >> 1]); };
+    // 64 rows or columns in eight steps, in the order in which products want them
+    auto read_a = [&](int k8, int f, v4i(&v)[4][2]) { ra.read(f + (k8 & 3), k8 >> 2, v[k8 & 3][k8 >> 2]); };
+    auto read_b = [&](int k8, v4i(&v)[4][2]) { rb.read(4 * wave + (k8 & 3), k8 >> 2, v[k8 & 3][k8 >> 2]); };
 
     if (ns > 0) {
         ra.at = slot_at(stage);
@@ -448,17 +455,17 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
         const HgIssue<G> issue_b(p, c, l, true, stage & 1), issue_a(p, c, l, false, stage & 1);
         if constexpr (copies.value)
             if (NP == 2) hg_all(issue_b);
-        v4i na[2][4] = {}, nw[2][4] = {};
+        v4i na[4][2] = {}, nw[4][2] = {};
         auto shift = [&]() {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) a[i][h] = na[i][h];
+                for (int h = 0; h < 2; ++h) a[i][h] = na[i][h];
         };
 #pragma unroll
         for (int pair = 0; pair + 1 < NP / 2; ++pair) {
             multiply(pair, [&](int i) {
-                if ((i & 1) == 0) read_a(i / 2, 2 * (pair + 1), na);
+                if ((i & 1) == 0) read_a(i / 2, 4 * (pair + 1), na);
                 if constexpr (copies.value) {
                     if (pair == 0 && i < 8) read_route(stage + 2, i);
                     const int at = 16 * pair + i - FROM;
@@ -485,9 +492,9 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
             fetch_stage_routes(stage + 4);
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int h = 0; h < 4; ++h) w[j][h] = nw[j][h];
+            for (int h = 0; h < 2; ++h) w[j][h] = nw[j][h];
         shift();
         ++stage;
     };
@@ -499,77 +506,71 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
 
     // the last product's result is there after 18 wait states
     asm volatile("s_nop 15\n\ts_nop 15");
-    const int r = lane & 31, g = lane >> 5;
-    const int n0 = t.nblk * G::COLS + wave * 32 * J;
+    const int r = lane & 15, g = lane >> 4;
+    const int n0 = t.nblk * G::COLS + wave * 16 * J;
     const size_t out_row = G::WEIGHTS ? (size_t)t.e * p.M + t.row0 : (size_t)t.row0;
     if (G::WEIGHTS && (p.accumulate || p.c_type == kFp32)) {
         // four columns a lane, in fp32 or added to what is there
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
+        for (int i = 0; i < 2 * NP; ++i) {
             __builtin_amdgcn_sched_barrier(0);
-            const int row = 32 * i + r;
+            const int row = 16 * i + r;
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+                float y[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float y[4];
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) y[v] = hg_sum(acc[i][j][4 * q + v]);
-                    const int col = n0 + 32 * j + 8 * q + 4 * g;
-                    if (row >= t.rows || col >= p.N) continue;
-                    const size_t at = (out_row + row) * p.N + col;
-                    if (p.c_type == kFp32) {
-                        float4 *o = reinterpret_cast<float4 *>((float *)p.c + at);
-                        float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (p.accumulate) old = *o;
-                        *o = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
-                    } else {
-                        uint2 *o = reinterpret_cast<uint2 *>((uint16_t *)p.c + at);
-                        const uint2 old = *o;
-                        typedef Element<T> L;
-                        *o = make_uint2(L::pack(L::lo(old.x) + y[0], L::hi(old.x) + y[1]),
-                                        L::pack(L::lo(old.y) + y[2], L::hi(old.y) + y[3]));
-                    }
+                for (int v = 0; v < 4; ++v) y[v] = hg_sum(acc[i][j][v]);
+                const int col = n0 + 16 * j + 4 * g;
+                if (row >= t.rows || col >= p.N) continue;
+                const size_t at = (out_row + row) * p.N + col;
+                if (p.c_type == kFp32) {
+                    float4 *o = reinterpret_cast<float4 *>((float *)p.c + at);
+                    float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (p.accumulate) old = *o;
+                    *o = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
+                } else {
+                    uint2 *o = reinterpret_cast<uint2 *>((uint16_t *)p.c + at);
+                    const uint2 old = *o;
+                    typedef Element<T> L;
+                    *o = make_uint2(L::pack(L::lo(old.x) + y[0], L::hi(old.x) + y[1]),
+                                    L::pack(L::lo(old.y) + y[2], L::hi(old.y) + y[3]));
                 }
+            }
         }
         return;
     }
-    // Four columns a lane, rounded; then lanes l and l + 32 exchange halves of two such groups, so
+    // Four columns a lane, rounded; then lanes l and l ^ 16 exchange halves of two such fragments, so
     // that each holds eight columns in a row and stores 16 bytes.
-    uint2 out[NP][J][4];
+    uint2 out[2 * NP][J];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
+    for (int i = 0; i < 2 * NP; ++i) {
         __builtin_amdgcn_sched_barrier(0);  // a few sums at a time leave the accumulators
-        const float weight = G::SWIGLU && p.probs ? l.weight[k % 3 * kHgTile + 32 * i + r] : 1.0f;
+        const float weight = G::SWIGLU && p.probs ? l.weight[k % 3 * kHgTile + 16 * i + r] : 1.0f;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int j = 0; j < J; ++j) {
+            float y[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float y[4];
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    y[v] = G::SWIGLU ? weight * hg_silu_times(hg_sum(acc[i][0][4 * q + v]), hg_sum(acc[i][1][4 * q + v]))
-                                     : hg_sum(acc[i][j][4 * q + v]);
-                out[i][j][q] = make_uint2(Element<T>::pack(y[0], y[1]), Element<T>::pack(y[2], y[3]));
-                // rounded here, not in the blocks of the stores: half the registers
-                asm volatile("" : "+v"(out[i][j][q].x), "+v"(out[i][j][q].y));
-            }
+            for (int v = 0; v < 4; ++v)
+                y[v] = G::SWIGLU ? weight * hg_silu_times(hg_sum(acc[i][j][v]), hg_sum(acc[i][(j + 2) & 3][v]))
+                                 : hg_sum(acc[i][j][v]);
+            out[i][j] = make_uint2(Element<T>::pack(y[0], y[1]), Element<T>::pack(y[2], y[3]));
+            // rounded here, not in the blocks of the stores: half the registers
+            asm volatile("" : "+v"(out[i][j].x), "+v"(out[i][j].y));
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const int row = 32 * i + r;
+    for (int i = 0; i < 2 * NP; ++i) {
+        const int row = 16 * i + r;
         uint16_t *crow = (uint16_t *)p.c + (out_row + row) * p.N;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-                const auto x = __builtin_amdgcn_permlane32_swap(out[i][j][q].x, out[i][j][q + 1].x, false, false);
-                const auto y = __builtin_amdgcn_permlane32_swap(out[i][j][q].y, out[i][j][q + 1].y, false, false);
-                const int col = n0 + 32 * j + 8 * (q + g);
-                if (row < t.rows && col < p.N)
-                    *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
-            }
+        for (int j = 0; j < J; j += 2) {
+            const auto x = __builtin_amdgcn_permlane16_swap(out[i][j].x, out[i][j + 1].x, false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(out[i][j].y, out[i][j + 1].y, false, false);
+            const int col = n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
+            if (row < t.rows && col < p.N)
+                *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+        }
     }
 }
 
@@ -695,8 +696,10 @@ hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_co
         if (b) hg_launch<HgGeom<kHalfRows, kBf16, false>>(p, cu_count, stream);
         else hg_launch<HgGeom<kHalfRows, kFp16, false>>(p, cu_count, stream);
     } else {
-        if (b) hg_launch<HgGeom<kHalfWeights, kBf16, false>>(p, cu_count, stream);
-        else hg_launch<HgGeom<kHalfWeights, kFp16, false>>(p, cu_count, stream);
+        if (p.gather == 1 && b) hg_launch<HgGeom<kHalfWeights, kBf16, false, 1>>(p, cu_count, stream);
+        else if (p.gather == 1) hg_launch<HgGeom<kHalfWeights, kFp16, false, 1>>(p, cu_count, stream);
+        else if (b) hg_launch<HgGeom<kHalfWeights, kBf16, false, 2>>(p, cu_count, stream);
+        else hg_launch<HgGeom<kHalfWeights, kFp16, false, 2>>(p, cu_count, stream);
     }
     return hipGetLastError();
 }

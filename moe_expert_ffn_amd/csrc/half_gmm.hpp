@@ -15,11 +15,11 @@ __device__ __forceinline__ int hg_row_end(const HalfGmmParams &p, int e) {
     return v < 0 ? 0 : v > p.R ? p.R : v;
 }
 
-// The token of a sorted route: what lies past the valid rows stays in bounds.
-__device__ __forceinline__ uint32_t hg_route(const HalfGmmParams &p, int v) { return v < 0 ? 0 : v < p.R ? v : p.R - 1; }
+// A sorted route and its token: what lies past the valid rows stays in bounds.
+__device__ __forceinline__ uint32_t hg_route(const HalfGmmParams &p, int v) { return min(max(v, 0), p.R - 1); }
 __device__ __forceinline__ uint32_t hg_token(const HalfGmmParams &p, int v) {
     const uint32_t u = hg_route(p, v);
-    return p.top_k == 1 ? u : __umulhi(u, p.top_k_inv);
+    return __umulhi(u, p.top_k_inv) + (u & p.one_k);
 }
 
 // silu(u) * g for a result that is rounded to 16 bits: the reciprocal's last ulp is not corrected

@@ -293,9 +293,10 @@ int run_half_gmm(const megamoe_dims &d, int kind, bool first, const uint16_t *a,
                  const float *probs, bool swiglu, void *c, int c_type, bool accumulate,
                  hipStream_t s) {
     const int inner = first && !swiglu ? 2 * d.I : d.I, wide = first ? 2 * d.I : d.I;
+    // the reciprocal: see run_mxfp4_gmm
     HalfGmmParams p{a, b, route, cumsum, probs, c, d.M * d.top_k, d.E, 0, 0, 0, d.top_k,
-                    (uint32_t)(((1ull << 32) + d.top_k - 1) / d.top_k),  // see run_mxfp4_gmm
-                    gather, swiglu, accumulate, c_type};
+                    d.top_k == 1 ? 0 : (uint32_t)(((1ull << 32) + d.top_k - 1) / d.top_k),
+                    d.top_k == 1 ? ~0u : 0u, gather, swiglu, accumulate, c_type};
     if (kind == kHalfWeights) {
         p.M = first ? wide : d.K;
         p.N = first ? d.K : wide;
@@ -305,6 +306,12 @@ int run_half_gmm(const megamoe_dims &d, int kind, bool first, const uint16_t *a,
         p.K = to_inner ? d.K : inner;
     }
     return hip_status(launch_half_gmm(p, kind, type, cu_count_current(), s));
+}
+
+// The weights' gradients look past a group's end by less than 64 rows, at byte offsets below 2^32.
+bool half_wgrad_ok(const megamoe_dims &d) {
+    const long long wide = d.K > 2 * d.I ? d.K : 2 * d.I;
+    return ((long long)d.M * d.top_k + 64) * wide < (1ll << 31);
 }
 
 // workspace of the 16-bit forward
@@ -812,6 +819,7 @@ int megamoe_half_gmm1_wgrad(const megamoe_dims *d, const uint16_t *dc, const uin
     for (const void *p : ptrs)
         if (!aligned16(p)) return MEGAMOE_EINVAL;
     if (!half_type(type) || (dw_type != type && dw_type != MEGAMOE_FP32)) return MEGAMOE_EINVAL;
+    if (!half_wgrad_ok(*d)) return MEGAMOE_EUNSUPPORTED;
     return run_half_gmm(*d, kHalfWeights, true, dc, x, type, sorted_route, 2, expert_cumsum,
                         nullptr, false, dw1, dw_type, accumulate != 0, (hipStream_t)stream);
 }
@@ -824,6 +832,7 @@ int megamoe_half_gmm2_wgrad(const megamoe_dims *d, const uint16_t *dout, const u
     for (const void *p : ptrs)
         if (!aligned16(p)) return MEGAMOE_EINVAL;
     if (!half_type(type) || (dw_type != type && dw_type != MEGAMOE_FP32)) return MEGAMOE_EINVAL;
+    if (!half_wgrad_ok(*d)) return MEGAMOE_EUNSUPPORTED;
     return run_half_gmm(*d, kHalfWeights, false, dout, y, type, sorted_route, 1, expert_cumsum,
                         nullptr, false, dw2, dw_type, accumulate != 0, (hipStream_t)stream);
 }

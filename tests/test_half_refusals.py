@@ -70,6 +70,14 @@ def test_pointers_types_and_dims(name):
         assert call(name, d=bad) == code
 
 
+def test_weight_gradients_limit():
+    """Their rows end 64 rows before the other entry points' do."""
+    d = MM.dims((1 << 31) // 32768 - 64, 32768, 8, 1, 128)
+    assert MM.megamoe_check_dims(d) == 0
+    for name in ("megamoe_half_gmm1_wgrad", "megamoe_half_gmm2_wgrad"):
+        assert call(name, d=d) == 2
+
+
 def test_workspaces():
     lib = MM.load()
     for name, size in (("megamoe_sort_routes", MM.megamoe_permute_workspace_bytes(D)),
