@@ -42,10 +42,12 @@ __device__ __forceinline__ v4f hg_mfma(v4i w, v4i a, v4f acc) {
 //            transposing LDS load, which gives a lane four values of one column.
 // Either way the 16-byte pieces are placed so that a fragment's reads meet every LDS bank equally often.
 //
-// A wave multiplies by columns that it has copied itself, and has all of a stage's in registers when the stage
-// begins: those of the stage after the next are copied from then on.  The barrier between two stages lies
-// before the last rows of the first are multiplied: they are in registers by then, so behind it the rows
-// of the stage after the next are copied, and the first fragments of the next one are read.
+// A stage is multiplied 64 rows at a time, in two phases of 32 of the reduction; what a phase multiplies is read from
+// LDS during the one before, into the registers that were free by then, so that nothing is moved between registers.
+// A wave multiplies by columns that it has copied itself: all of a stage's are in registers after the first
+// phase, and from then on those of the stage after the next are copied.  The barrier between two stages lies
+// before the last phase of the first: its rows are in registers by then, so behind it the rows of
+// the stage after the next are copied, and the first fragments of the next one are read.
 //
 // The grid is persistent, and the copies run two stages ahead of the products through the workgroup's
 // tiles, so that a tile's first stages are there when the tile before has been rounded and stored.
@@ -323,7 +325,7 @@ __device__ __forceinline__ float hg_sum(float a) {
 template <typename G>
 struct HgRun {
     const HalfGmmParams &p;
-    const HgLds &l;
+    const HgLds l;  // (a reference to it was kept in LDS, and its pointers taken for generic ones)
     const HgTile *list;
     int n;             // tiles of this workgroup
     int stage, total;  // of all of the workgroup's: the one that is multiplied next, and how many there are
@@ -332,6 +334,7 @@ struct HgRun {
     int route_k, route_s, route_left;  // weights: the next stage whose routes are copied
     HgRead<G::A_ACROSS> ra;
     HgRead<G::B_ACROSS> rb;
+    v4i w[4][2], a[4][2];  // columns of the stage, the 64 rows that are multiplied: of both phases
 
     __device__ __forceinline__ HgTile tile(int k) const { return hg_uniform(list[k & (kHgList - 1)]); }
     __device__ __forceinline__ static int stages(const HgTile &t) { return (t.red + kHgK - 1) / kHgK; }
@@ -357,6 +360,17 @@ struct HgRun {
         }
         ++route_s;
         --route_left;
+    }
+    __device__ __forceinline__ const uint8_t *slot(int g) const { return l.data + (g & 1) * 2 * kHgOperand; }
+    // the first phase's fragments of stage g, in eight steps
+    __device__ __forceinline__ void read_first(int g, int k) {
+        if (k & 1) {
+            ra.at = slot(g);
+            ra.read(k >> 1, 0, a[k >> 1][0]);
+        } else {
+            rb.at = slot(g) + kHgOperand;
+            rb.read(4 * __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) + (k >> 1), 0, w[k >> 1][0]);
+        }
     }
     // before the copies of a stage, and behind them
     __device__ __forceinline__ void open() {
@@ -406,22 +420,19 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
     const int ns = (t.red + kHgK - 1) / kHgK;
 
     v4f acc[2 * NP][4] = {};
-    v4i w[4][2], a[4][2];  // columns of the stage, the 64 rows that are multiplied
-    // between(k) comes after every other of the 32 products: reads and copies there, one or two at a time, as a batch
+    // between(k) comes after the k-th of its 16 products: reads and copies there, one or two at a time, as a batch
     // of either holds the products up while it is taken in.
-    auto multiply = [&](int pair, auto between) {
+    auto phase = [&](int pair, int h, auto between) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v4f &d = acc[4 * pair + i][j];
-                    d = hg_mfma<T>(w[j][h], a[i][h], d);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (j & 1) between(8 * h + 2 * i + (j >> 1));
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int j = 0; j < 4; ++j) {
+                v4f &d = acc[4 * pair + i][j];
+                d = hg_mfma<T>(w[j][h], a[i][h], d);
+                __builtin_amdgcn_sched_barrier(0);
+                between(4 * i + j);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         // the sums are wanted here: without this the compiler puts a stage's products together
         // behind its barrier and copies, where the reads no longer overlap them
 #pragma unroll
@@ -429,80 +440,61 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
 #pragma unroll
             for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[4 * pair + i][j]));
     };
-    auto slot_at = [&](int g) { return l.data + (g & 1) * 2 * kHgOperand; };
-    // 64 rows or columns in eight steps, in the order in which products want them
-    auto read_a = [&](int k8, int f, v4i(&v)[4][2]) { ra.read(f + (k8 & 3), k8 >> 2, v[k8 & 3][k8 >> 2]); };
-    auto read_b = [&](int k8, v4i(&v)[4][2]) { rb.read(4 * wave + (k8 & 3), k8 >> 2, v[k8 & 3][k8 >> 2]); };
-
-    if (ns > 0) {
-        ra.at = slot_at(stage);
-        rb.at = slot_at(stage) + kHgOperand;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            read_b(i, w);
-            read_a(i, 0, a);
-        }
-    }
     // The copies are spread over a stage, as four waves make them at once and a copy takes longer to be taken in
-    // than a product: those of the columns over the products before the barrier, those of the rows over the
-    // rest.  (In eight slots in a row each: 5% slower.)
-    constexpr int FROM = G::WEIGHTS ? 8 : 1, EVERY = NP == 8 ? (G::WEIGHTS ? 5 : 6) : NP == 6 ? 4 : G::WEIGHTS ? 1 : 2;
-    auto one_stage = [&](int s, auto copies) {
-        ra.at = slot_at(stage);
-        // the stage's columns are in registers, and their place is free
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // than a product: those of the columns over the phases before the barrier, those of the rows over
+    // the one behind it.
+    constexpr int LAST = NP / 2 - 1, FROM = G::WEIGHTS ? 8 : 1, EVERY = LAST ? (32 * LAST - FROM) / 8 : 1;
+    auto one_stage = [&](auto copies) {  // copies: stage `stage` + 2 is to be copied
         if constexpr (copies.value) open();
-        const HgIssue<G> issue_b(p, c, l, true, stage & 1), issue_a(p, c, l, false, stage & 1);
-        if constexpr (copies.value)
-            if (NP == 2) hg_all(issue_b);
-        v4i na[4][2] = {}, nw[4][2] = {};
-        auto shift = [&]() {
+        const HgIssue<G> columns(p, c, l, true, stage & 1), rows(p, c, l, false, stage & 1);
+        ra.at = slot(stage);
+        rb.at = slot(stage) + kHgOperand;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) a[i][h] = na[i][h];
-        };
-#pragma unroll
-        for (int pair = 0; pair + 1 < NP / 2; ++pair) {
-            multiply(pair, [&](int i) {
-                if ((i & 1) == 0) read_a(i / 2, 4 * (pair + 1), na);
+        for (int pair = 0; pair <= LAST; ++pair) {
+            phase(pair, 0, [&](int k) {
+                if (k < 8 && !(k & 1)) ra.read(4 * pair + (k >> 1), 1, a[k >> 1][1]);
+                if (pair == 0 && k < 8 && (k & 1)) rb.read(4 * wave + (k >> 1), 1, w[k >> 1][1]);
                 if constexpr (copies.value) {
-                    if (pair == 0 && i < 8) read_route(stage + 2, i);
-                    const int at = 16 * pair + i - FROM;
-                    if (at >= 0 && at % EVERY == 0 && at / EVERY < 8) issue_b.copy(at / EVERY);
+                    const int at = 32 * pair + k - 16 - FROM;
+                    if (LAST && pair && at >= 0 && at % EVERY == 0 && at / EVERY < 8) columns.copy(at / EVERY);
                 }
             });
-            shift();
+            if (pair == 0) {
+                // the stage's columns are in registers, and their place is free
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if constexpr (copies.value)
+                    if (LAST == 0) hg_all(columns);
+            }
+            if (pair == LAST && (copies.value || stage + 1 < total)) {
+                // all but the columns of the stage after the next
+                wait_vmcnt<copies.value ? 8 : 0>();
+                __syncthreads();
+            }
+            phase(pair, 1, [&](int k) {
+                if (pair < LAST) {
+                    if (k < 8 && !(k & 1)) ra.read(4 * (pair + 1) + (k >> 1), 0, a[k >> 1][0]);
+                } else if (k < 8) {
+                    read_first(stage + 1, k);
+                }
+                if constexpr (copies.value) {
+                    if (LAST && pair == 0 && k < 8) read_route(stage + 2, k);
+                    const int at = 32 * pair + k - FROM;
+                    if (LAST && pair < LAST && at >= 0 && at % EVERY == 0 && at / EVERY < 8) columns.copy(at / EVERY);
+                    if (pair == LAST && (k & 1)) rows.copy(k >> 1);
+                }
+            });
         }
-        if (copies.value || stage + 1 < total) {
-            // all but the columns of the stage after the next
-            wait_vmcnt<copies.value ? 8 : 0>();
-            __syncthreads();
-        }
-        ra.at = slot_at(stage + 1);
-        rb.at = slot_at(stage + 1) + kHgOperand;
-        multiply(NP / 2 - 1, [&](int i) {
-            if (i & 1) read_a(i / 2, 0, na);
-            else read_b(i / 2, nw);
-            if constexpr (copies.value)
-                if (i & 1) issue_a.copy(i / 2);
-        });
         if constexpr (copies.value) {
             close();
             fetch_stage_routes(stage + 4);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) w[j][h] = nw[j][h];
-        shift();
         ++stage;
     };
     const int with_copies = min(ns, max(0, total - 2 - stage));
 #pragma unroll 1
-    for (int s = 0; s < with_copies; ++s) one_stage(s, std::true_type{});
+    for (int s = 0; s < with_copies; ++s) one_stage(std::true_type{});
 #pragma unroll 1
-    for (int s = with_copies; s < ns; ++s) one_stage(s, std::false_type{});
+    for (int s = with_copies; s < ns; ++s) one_stage(std::false_type{});
 
     // the last product's result is there after 18 wait states
     asm volatile("s_nop 15\n\ts_nop 15");
@@ -541,35 +533,39 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
     }
     // Four columns a lane, rounded; then lanes l and l ^ 16 exchange halves of two such fragments, so
     // that each holds eight columns in a row and stores 16 bytes.
-    uint2 out[2 * NP][J];
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-        __builtin_amdgcn_sched_barrier(0);  // a few sums at a time leave the accumulators
-        const float weight = G::SWIGLU && p.probs ? l.weight[k % 3 * kHgTile + 16 * i + r] : 1.0f;
+    for (int pair = 0; pair < NP / 2; ++pair) {
+        uint2 out[4][J];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            float y[4];
+        for (int i = 0; i < 4; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // a few sums at a time leave the accumulators
+            const int f = 4 * pair + i;
+            const float weight = G::SWIGLU && p.probs ? l.weight[k % 3 * kHgTile + 16 * f + r] : 1.0f;
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-                y[v] = G::SWIGLU ? weight * hg_silu_times(hg_sum(acc[i][j][v]), hg_sum(acc[i][(j + 2) & 3][v]))
-                                 : hg_sum(acc[i][j][v]);
-            out[i][j] = make_uint2(Element<T>::pack(y[0], y[1]), Element<T>::pack(y[2], y[3]));
-            // rounded here, not in the blocks of the stores: half the registers
-            asm volatile("" : "+v"(out[i][j].x), "+v"(out[i][j].y));
+            for (int j = 0; j < J; ++j) {
+                float y[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    y[v] = G::SWIGLU ? weight * hg_silu_times(hg_sum(acc[f][j][v]), hg_sum(acc[f][(j + 2) & 3][v]))
+                                     : hg_sum(acc[f][j][v]);
+                out[i][j] = make_uint2(Element<T>::pack(y[0], y[1]), Element<T>::pack(y[2], y[3]));
+                // rounded here, not in the blocks of the stores: half the registers
+                asm volatile("" : "+v"(out[i][j].x), "+v"(out[i][j].y));
+            }
         }
-    }
-    __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-        const int row = 16 * i + r;
-        uint16_t *crow = (uint16_t *)p.c + (out_row + row) * p.N;
+        for (int i = 0; i < 4; ++i) {
+            const int row = 64 * pair + 16 * i + r;
+            uint16_t *crow = (uint16_t *)p.c + (out_row + row) * p.N;
 #pragma unroll
-        for (int j = 0; j < J; j += 2) {
-            const auto x = __builtin_amdgcn_permlane16_swap(out[i][j].x, out[i][j + 1].x, false, false);
-            const auto y = __builtin_amdgcn_permlane16_swap(out[i][j].y, out[i][j + 1].y, false, false);
-            const int col = n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
-            if (row < t.rows && col < p.N)
-                *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+            for (int j = 0; j < J; j += 2) {
+                const auto x = __builtin_amdgcn_permlane16_swap(out[i][j].x, out[i][j + 1].x, false, false);
+                const auto y = __builtin_amdgcn_permlane16_swap(out[i][j].y, out[i][j + 1].y, false, false);
+                const int col = n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
+                if (row < t.rows && col < p.N)
+                    *reinterpret_cast<uint4 *>(crow + col) = make_uint4(x[0], y[0], x[1], y[1]);
+            }
         }
     }
 }
@@ -648,6 +644,8 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     if (stages > 1) wait_vmcnt<16>();
     else wait_vmcnt<0>();
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) run.read_first(0, i);
     for (int k = 0; k < n; ++k) {
         if (k > 0 && k % (kHgList / 2) == 0) {
             __syncthreads();  // nobody looks at the older half any more: tiles without stages have no barrier
