@@ -75,33 +75,38 @@ struct HgTile {
 };
 
 struct HgSchedule {
-    int pre[kHgE + 1];  // products: tiles of the experts before e
     int first[kHgE], rows[kHgE];
-    int order[kHgE];    // weights: experts, most rows first
+    int order[kHgE];    // experts, those with the longest tiles first
+    int pre[kHgE + 1];  // products: tiles of the experts before the i-th of them
     int total;
 };
 
-// Products: tiles by expert, column block and row block, an expert's rows split evenly over its row blocks in
-// units of 32.  Weights: every expert has as many tiles, those of the largest groups first.
+// Tiles by expert, those whose tiles take longest first: weights: that have most rows; products: most
+// rows in a tile.  Weights: every expert has as many tiles.  Products: an expert's rows are split evenly
+// over its row blocks in units of 32.
 template <typename G>
 __device__ __forceinline__ void hg_schedule(const HalfGmmParams &p, int *s_w, HgSchedule &s) {
     const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
     const int first = e < p.E ? hg_row_end(p, e - 1) : 0;
     const int rows = e < p.E ? max(0, hg_row_end(p, e) - first) : 0;
+    const int blocks = (rows + kHgTile - 1) / kHgTile;
+    const int length = G::WEIGHTS || rows == 0 ? rows : (rows + blocks - 1) / blocks;
     s.first[e] = first;
     s.rows[e] = rows;
+    s.pre[e] = length;
+    __syncthreads();
+    int rank = 0;
+    for (int i = 0; i < p.E; ++i) {
+        const int other = s.pre[i];
+        rank += other > length || (other == length && i < e);
+    }
+    if (e >= p.E) rank = e;
+    s.order[rank] = e;
     if constexpr (G::WEIGHTS) {
-        __syncthreads();
-        int rank = 0;
-        for (int i = 0; i < p.E; ++i) {
-            const int other = s.rows[i];
-            rank += other > rows || (other == rows && i < e);
-        }
-        if (e < p.E) s.order[rank] = e;
-        if (e == 0)
-            s.total = p.E * ((p.M + kHgTile - 1) / kHgTile) * ((p.N + kHgTile - 1) / kHgTile);
+        if (e == 0) s.total = p.E * ((p.M + kHgTile - 1) / kHgTile) * ((p.N + kHgTile - 1) / kHgTile);
     } else {
-        const int tiles = (rows + kHgTile - 1) / kHgTile * ((p.N + G::COLS - 1) / G::COLS);
+        __syncthreads();
+        const int tiles = (s.rows[s.order[e]] + kHgTile - 1) / kHgTile * ((p.N + G::COLS - 1) / G::COLS);
         const int incl = wave_inclusive_scan(tiles);
         if (lane == kWave - 1) s_w[wave] = incl;
         __syncthreads();
@@ -121,13 +126,13 @@ __device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgS
         const int e = s.order[t / (mb * nb)], local = t % (mb * nb), m0 = local % mb * kHgTile;
         return HgTile{e, m0, min(kHgTile, p.M - m0), local / mb, s.first[e], s.rows[e]};
     } else {
-        int lo = 0, hi = kHgE - 1;  // the first expert that ends after t
+        int lo = 0, hi = kHgE - 1;  // the first of the order that ends after t
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (s.pre[mid + 1] > t) hi = mid;
             else lo = mid + 1;
         }
-        const int rows = s.rows[lo], local = t - s.pre[lo];
+        const int e = s.order[lo], rows = s.rows[e], local = t - s.pre[lo];
         // eight row blocks, then the columns, then the next eight: what an XCD's workgroups multiply at one time
         // shares most (16 row blocks, us: row gradient 1668 -> 1594, product 1602 -> 1590)
         const int mb = (rows + kHgTile - 1) / kHgTile, nb = (p.N + G::COLS - 1) / G::COLS;
@@ -135,7 +140,7 @@ __device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgS
         const int m = 8 * run + in % wide;
         const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
         const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
-        return HgTile{lo, s.first[lo] + 32 * u0, min(rows, 32 * u1) - 32 * u0, in / wide, 0, p.K};
+        return HgTile{e, s.first[e] + 32 * u0, min(rows, 32 * u1) - 32 * u0, in / wide, 0, p.K};
     }
 }
 __device__ __forceinline__ HgTile hg_uniform(const HgTile &x) {
@@ -582,26 +587,30 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
 
     hg_schedule<G>(p, s_w, s_s);
     const int total = __builtin_amdgcn_readfirstlane(s_s.total), tid = threadIdx.x;
-    // Workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share blocks of rows and
-    // columns in its L2.  Weights: a run of every round of tiles, every other one backwards, as
-    // tiles get shorter.
-    const int groups = gridDim.x >> 3, xcd = blockIdx.x & 7, in = blockIdx.x >> 3;
-    const int per = (total + 7) / 8, t0 = xcd * per + in, t1 = min(xcd * per + per, total);
-    const int v0 = xcd * groups + in, v1 = (int)gridDim.x - 1 - v0;
-    int n;
-    if (G::WEIGHTS) {
-        const int rounds = total / (int)gridDim.x, rest = total - rounds * (int)gridDim.x;
-        n = rounds + ((rounds & 1 ? v1 : v0) < rest);
-    } else {
-        n = t0 < t1 ? (t1 - t0 + groups - 1) / groups : 0;
+    // Rounds of a tile a workgroup, every other one backwards as tiles get shorter.  Workgroups go round the XCDs: those
+    // of an XCD take neighbouring tiles, which share blocks of rows and columns in its L2.  The tiles past whole
+    // rounds are an eighth an XCD: where all of an XCD's workgroups have one more and another's none, an
+    // XCD's share of the memory's rate is left idle.
+    const int groups = gridDim.x >> 3, round = gridDim.x;
+    const int rounds = total / round, rest = total - rounds * round;
+    auto place = [&](int i, int &xcd, int &in) {
+        xcd = i & 1 ? 7 - (blockIdx.x & 7) : blockIdx.x & 7;
+        in = i & 1 ? groups - 1 - (blockIdx.x >> 3) : blockIdx.x >> 3;
+    };
+    auto tile_of = [&](int i) {
+        int xcd, in;
+        place(i, xcd, in);
+        return hg_find_tile<G>(p, s_s, i * round + (i < rounds ? xcd * groups : rest * xcd / 8) + in);
+    };
+    int n = rounds;
+    {
+        int xcd, in;
+        place(rounds, xcd, in);
+        n += in < rest * (xcd + 1) / 8 - rest * xcd / 8;
     }
     if (n == 0) return;
     auto look_up = [&](int k) {  // half of the list, from tile k on
-        if (tid < kHgList / 2 && k + tid < n) {
-            const int i = k + tid;
-            s_t[i & (kHgList - 1)] =
-                hg_find_tile<G>(p, s_s, G::WEIGHTS ? i * (int)gridDim.x + (i & 1 ? v1 : v0) : t0 + i * groups);
-        }
+        if (tid < kHgList / 2 && k + tid < n) s_t[(k + tid) & (kHgList - 1)] = tile_of(k + tid);
     };
     look_up(0);
     look_up(kHgList / 2);
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
         __syncthreads();
         int mine = 0;
         for (int i = tid; i < n; i += kHgThreads)
-            mine += (hg_find_tile<G>(p, s_s, i * (int)gridDim.x + (i & 1 ? v1 : v0)).red + kHgK - 1) / kHgK;
+            mine += (tile_of(i).red + kHgK - 1) / kHgK;
         atomicAdd(&s_w[0], mine);  // of integers: in any order
         __syncthreads();
         stages = __builtin_amdgcn_readfirstlane(s_w[0]);
