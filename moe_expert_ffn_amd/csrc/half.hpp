@@ -51,7 +51,7 @@ struct NormParams {
     int M, K, top_k, R, gate_type, gate_rows, gate_cols, h_type;
     float alpha, eps;
 };
-int norm_grad_groups(int M);
+int norm_grad_groups(int M, int K);
 hipError_t launch_norm(const NormParams &p, int x_type, int rows_type, bool grad, hipStream_t stream);
 
 // The router's gradient (route_grad.hip).

@@ -923,7 +923,7 @@ int megamoe_norm(const megamoe_dims *d, const void *x, int x_type, const void *r
 int megamoe_norm_grad_workspace_bytes(const megamoe_dims *d, size_t *bytes) {
     MEGAMOE_TRY(megamoe_check_dims(d));
     if (!bytes) return MEGAMOE_EINVAL;
-    *bytes = (size_t)3 * norm_grad_groups(d->M) * d->K * sizeof(float);
+    *bytes = (size_t)3 * norm_grad_groups(d->M, d->K) * d->K * sizeof(float);
     return MEGAMOE_OK;
 }
 
