@@ -119,12 +119,23 @@ __device__ __forceinline__ void hg_schedule(const HalfGmmParams &p, int *s_w, Hg
     __syncthreads();
 }
 
+// Tile `local` of mb row blocks by nb column blocks: eight row blocks, then the columns, then the next eight: what an
+// XCD's workgroups multiply at one time shares most (16 row blocks in turn, us: row gradient 1668 for 1594, product
+// 1602 for 1590, weights' gradient of 16 groups of 2048 rows 990 for 975).
+__device__ __forceinline__ void hg_block(int local, int mb, int nb, int &m, int &n) {
+    const int run = local / (8 * nb), wide = min(8, mb - 8 * run), in = local - 8 * nb * run;
+    m = 8 * run + in % wide;
+    n = in / wide;
+}
+
 template <typename G>
 __device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgSchedule &s, int t) {  // t < total
+    const int nb = (p.N + G::COLS - 1) / G::COLS;
+    int m, n;
     if constexpr (G::WEIGHTS) {
-        const int mb = (p.M + kHgTile - 1) / kHgTile, nb = (p.N + kHgTile - 1) / kHgTile;
-        const int e = s.order[t / (mb * nb)], local = t % (mb * nb), m0 = local % mb * kHgTile;
-        return HgTile{e, m0, min(kHgTile, p.M - m0), local / mb, s.first[e], s.rows[e]};
+        const int mb = (p.M + kHgTile - 1) / kHgTile, e = s.order[t / (mb * nb)];
+        hg_block(t % (mb * nb), mb, nb, m, n);
+        return HgTile{e, m * kHgTile, min(kHgTile, p.M - m * kHgTile), n, s.first[e], s.rows[e]};
     } else {
         int lo = 0, hi = kHgE - 1;  // the first of the order that ends after t
         while (lo < hi) {
@@ -132,15 +143,11 @@ __device__ __forceinline__ HgTile hg_find_tile(const HalfGmmParams &p, const HgS
             if (s.pre[mid + 1] > t) hi = mid;
             else lo = mid + 1;
         }
-        const int e = s.order[lo], rows = s.rows[e], local = t - s.pre[lo];
-        // eight row blocks, then the columns, then the next eight: what an XCD's workgroups multiply at one time
-        // shares most (16 row blocks, us: row gradient 1668 -> 1594, product 1602 -> 1590)
-        const int mb = (rows + kHgTile - 1) / kHgTile, nb = (p.N + G::COLS - 1) / G::COLS;
-        const int run = local / (8 * nb), wide = min(8, mb - 8 * run), in = local - 8 * nb * run;
-        const int m = 8 * run + in % wide;
+        const int e = s.order[lo], rows = s.rows[e], mb = (rows + kHgTile - 1) / kHgTile;
+        hg_block(t - s.pre[lo], mb, nb, m, n);
         const int nu = (rows + 31) / 32, q = nu / mb, r = nu % mb;
         const int u0 = m * q + min(m, r), u1 = u0 + q + (m < r);
-        return HgTile{e, s.first[e] + 32 * u0, min(rows, 32 * u1) - 32 * u0, in / wide, 0, p.K};
+        return HgTile{e, s.first[e] + 32 * u0, min(rows, 32 * u1) - 32 * u0, n, 0, p.K};
     }
 }
 __device__ __forceinline__ HgTile hg_uniform(const HgTile &x) {
