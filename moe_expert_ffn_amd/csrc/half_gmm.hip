@@ -161,6 +161,7 @@ struct HgLds {
     uint32_t data_at;  // its LDS address
     int32_t *route;    // products: [2][256] routes of a tile's rows; weights: [kHgRing][64] routes of a stage
     float *weight;     // products with SwiGLU: [3][256] weights of a tile's rows
+    uint32_t *row;     // weights: [4][64] byte offsets of a stage's gathered rows, of each wave
     uint32_t route_at, weight_at;
 };
 
@@ -193,10 +194,10 @@ struct HgCopies {
     uint32_t step_b;
     // weights: rows past the group are out of the buffers' bounds and read as 0
     v4i ra, rb;
-    uint32_t gathered;     // byte of the lane's columns in a gathered row, in even copies
-    uint32_t straight[2];  // byte offset of the lane's first row in the other operand, in even and odd copies
-    int left;              // rows of the group from the lane's first one on
-    int tok[8];            // the routes of the lane's rows
+    uint32_t gathered[2];  // byte of the lane's columns in a gathered row, in even and odd copies
+    uint32_t straight[2];  // byte offset of the lane's first row in the other operand, likewise
+    int left;              // rows of the group from the stage's first one on
+    uint32_t row[8];       // byte offsets of the lane's gathered rows
 };
 
 // Byte of a lane's columns in its panel of columns from n0, of n that are a multiple of 128, in even copies; in odd
@@ -217,8 +218,9 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
     if constexpr (G::WEIGHTS) {
         const uint32_t ca = hg_across_column(t.row0 + wave * 64, p.M);
         const uint32_t cb = hg_across_column(t.nblk * kHgTile + wave * 64, p.N);
-        c.left = t.red - (lane >> 3);
-        c.gathered = G::GATHER == 1 ? ca : cb;
+        c.left = t.red;
+        c.gathered[0] = G::GATHER == 1 ? ca : cb;
+        c.gathered[1] = c.gathered[0] ^ 32;
         c.straight[0] = (uint32_t)(lane >> 3) * (2 * (G::GATHER == 1 ? p.N : p.M)) + (G::GATHER == 1 ? cb : ca);
         c.straight[1] = c.straight[0] ^ 32;
         const uint32_t la = 2 * p.M, lb = 2 * p.N, tokens = p.R / p.top_k;
@@ -249,12 +251,10 @@ __device__ __forceinline__ void hg_open(const HalfGmmParams &p, const HgTile &t,
 }
 
 // weights: the i-th copy's byte offset.  Rows past the group are not within the buffer of the straight
-// operand, whose bytes end with the group; a gathered row of theirs is put past the end.
+// operand, whose bytes end with the group; a gathered row of theirs lies past the end.
 template <typename G>
-__device__ __forceinline__ uint32_t hg_offset(const HalfGmmParams &p, const HgCopies<G> &c, int i, int operand, uint32_t ld) {
-    if (G::GATHER != operand) return c.straight[i & 1] + (uint32_t)i * (8 * ld);
-    const uint32_t v = hg_token(p, c.tok[i]) * ld + (c.gathered ^ (i & 1) * 32);
-    return 8 * i < c.left ? v : 0xffffff00u;  // an array has at most so many bytes
+__device__ __forceinline__ uint32_t hg_offset(const HgCopies<G> &c, int i, int operand, uint32_t ld) {
+    return G::GATHER == operand ? c.row[i] + c.gathered[i & 1] : c.straight[i & 1] + (uint32_t)i * (8 * ld);
 }
 
 template <typename G>
@@ -278,7 +278,7 @@ struct HgIssue {  // the copies of one operand's stage into slot `slot`
     }
     __device__ __forceinline__ void copy(int i) const {
         if constexpr (G::WEIGHTS) {
-            const uint32_t v = b ? hg_offset<G>(p, c, i, 2, 2 * p.N) : hg_offset<G>(p, c, i, 1, 2 * p.M);
+            const uint32_t v = b ? hg_offset<G>(c, i, 2, 2 * p.N) : hg_offset<G>(c, i, 1, 2 * p.M);
             dma16_buffer(rsrc, v, at + i * 1024);
         } else if (b) {
             dma16_nt(base, c.vb[i], at + i * 1024);
@@ -411,10 +411,20 @@ struct HgRun {
             c.b += c.step_b;
         }
     }
-    // weights: the route of the lane's rows of the i-th copies of stage `at`
-    __device__ __forceinline__ void read_route(int at, int i) {
-        if constexpr (G::WEIGHTS)
-            c.tok[i] = l.route[(at & (kHgRing - 1)) * kHgK + 8 * i + (int)((threadIdx.x & 63) >> 3)];
+    // weights: the byte offsets of the gathered rows of stage `at`, whose copies are next: a row a lane, and through
+    // LDS, in a place of the wave's own, to the lanes that copy the row
+    __device__ __forceinline__ int read_route(int at) const {
+        return l.route[(at & (kHgRing - 1)) * kHgK + (int)(threadIdx.x & 63)];
+    }
+    __device__ __forceinline__ void place_row(int route) const {
+        const uint32_t ld = 2 * (G::GATHER == 1 ? p.M : p.N);
+        // an array's bytes end 64 rows below 2^32
+        uint32_t v = hg_token(p, route) * ld;
+        asm volatile("" : "+v"(v));  // a choice, not a branch: one in a stage undoes its registers
+        l.row[threadIdx.x] = (int)(threadIdx.x & 63) < c.left ? v : 0u - 4 * ld;
+    }
+    __device__ __forceinline__ void read_row(int i) {
+        c.row[i] = l.row[(threadIdx.x & ~63) + 8 * i + (int)((threadIdx.x & 63) >> 3)];
     }
 
     // Multiplies tile t, of at most 32 NP rows, whose first stage is in LDS, copies two stages ahead,
@@ -461,12 +471,15 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
         const HgIssue<G> columns(p, c, l, true, stage & 1), rows(p, c, l, false, stage & 1);
         ra.at = slot(stage);
         rb.at = slot(stage) + kHgOperand;
+        int route;
 #pragma unroll
         for (int pair = 0; pair <= LAST; ++pair) {
             phase(pair, 0, [&](int k) {
                 if (k < 8 && !(k & 1)) ra.read(4 * pair + (k >> 1), 1, a[k >> 1][1]);
                 if (pair == 0 && k < 8 && (k & 1)) rb.read(4 * wave + (k >> 1), 1, w[k >> 1][1]);
                 if constexpr (copies.value) {
+                    if (G::WEIGHTS && pair == 0 && k == 8) route = read_route(stage + 2);
+                    if (G::WEIGHTS && pair == 0 && k == 14) place_row(route);
                     const int at = 32 * pair + k - 16 - FROM;
                     if (LAST && pair && at >= 0 && at % EVERY == 0 && at / EVERY < 8) columns.copy(at / EVERY);
                 }
@@ -489,7 +502,7 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
                     read_first(stage + 1, k);
                 }
                 if constexpr (copies.value) {
-                    if (LAST && pair == 0 && k < 8) read_route(stage + 2, k);
+                    if (G::WEIGHTS && pair == 0 && k < 8) read_row(k);
                     const int at = 32 * pair + k - FROM;
                     if (LAST && pair < LAST && at >= 0 && at % EVERY == 0 && at / EVERY < 8) columns.copy(at / EVERY);
                     if (pair == LAST && (k & 1)) rows.copy(k >> 1);
@@ -608,6 +621,7 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     __shared__ HgSchedule s_s;
     __shared__ HgTile s_t[kHgList];
     __shared__ int32_t s_route[2 * kHgTile];
+    __shared__ uint32_t s_row[G::WEIGHTS ? kHgThreads : 1];
     __shared__ float s_weight[G::SWIGLU ? 3 * kHgTile : 1];
     __shared__ __align__(16) uint8_t s_data[4 * kHgOperand];
     static_assert(kHgRing * kHgK <= 2 * kHgTile, "the ring of routes");
@@ -654,7 +668,7 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     }
     __syncthreads();
 
-    const HgLds l{s_data, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)), s_route, s_weight,
+    const HgLds l{s_data, (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_data)), s_route, s_weight, s_row,
                   (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_route)),
                   (uint32_t)__builtin_amdgcn_readfirstlane(lds_addr(s_weight))};
     HgRun<G> run{p, l, s_t, n};
@@ -671,8 +685,11 @@ __global__ __launch_bounds__(kHgThreads) __attribute__((amdgpu_waves_per_eu(1, 1
     __syncthreads();
     for (int i = 0; i < min(2, stages); ++i) {
         run.open();
+        if constexpr (G::WEIGHTS) {
+            run.place_row(run.read_route(i));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) run.read_route(i, j);
+            for (int j = 0; j < 8; ++j) run.read_row(j);
+        }
         hg_all(HgIssue<G>(p, run.c, l, true, i));
         hg_all(HgIssue<G>(p, run.c, l, false, i));
         run.close();
