@@ -13,7 +13,8 @@ issued before the current tile's epilogue, so copies are in flight almost
 everywhere.  The build therefore compiles the GEMM to assembly as well and
 fails if the kernel accesses scratch (spill) memory anywhere, or if an
 instantiation uses more registers or spills more values than recorded in
-GEMM_RESOURCES below.
+GEMM_RESOURCES below.  The 16-bit products copy in the same way, and their sums
+alone are half of the register file: the build fails where one of them spills.
 """
 from __future__ import annotations
 
@@ -115,6 +116,22 @@ def check_gemm_resources(remarks: str) -> list[str]:
     return problems
 
 
+def check_half_resources(remarks: str) -> list[str]:
+    """No instantiation of the 16-bit products spills a vector value."""
+    problems = []
+    found = 0
+    for name, r in kernel_resources(remarks).items():
+        if "half_gmm_kernel" not in name and "half_few_kernel" not in name:
+            continue
+        found += 1
+        spills, scratch = r.get("VGPRs Spill", 0), r.get("ScratchSize", 0)
+        if spills or scratch:
+            problems.append(f"16-bit product {name}: vector spills {spills}, scratch {scratch} bytes a lane")
+    if not found:
+        problems.append("no 16-bit product found in the resource report")
+    return problems
+
+
 def check_gemm_loops(asm: str) -> list[str]:
     """No scratch access in a GEMM kernel, and none inside a copy loop.
 
@@ -185,7 +202,7 @@ def build(verbose: bool = False) -> str:
     remarks = "\n".join(r for _, r in done)
     with open(os.path.join(BUILD, "resource_usage.txt"), "w") as f:
         f.write(remarks)
-    problems = check_gemm_resources(remarks) + check_gemm_loops(gemm_asm)
+    problems = check_gemm_resources(remarks) + check_half_resources(remarks) + check_gemm_loops(gemm_asm)
     if problems:
         raise RuntimeError("GEMM register guard failed:\n  " + "\n  ".join(problems))
     tmp = LIB + f".tmp{os.getpid()}"
