@@ -151,30 +151,33 @@ def _gate(gate: torch.Tensor | None, M: int, K: int, dev: int):
     return _at("gate", gate, None, None, dev), _type(gate), gate.shape[0], gate.shape[1]
 
 
-def _first(*tensors):
-    return next((t for t in tensors if t is not None), None)
-
-
 def megamoe_norm(d, x=None, rows=None, expanded_row_idx=None, w_after=None, gate=None, alpha=1.0,
                  w_before=None, eps=1e-6, s=None, r=None, h=None, stream=None):
     """s = rows[t], or summed over the token's routes; n = s / rms(s) * w_after, or s;
     r = x + alpha * gate * n; h = r / rms(r) * w_before.  s, r, h: outputs, those that are
     wanted.  x and r have one type, rows and s one, h its own."""
-    M, K, one, f32 = d.M, d.K, _first(x, rows), torch.float32
-    dev = _device(one)
+    # what is not there is passed by at once: at one token the call takes longer than the kernel
+    M, K, f32 = d.M, d.K, torch.float32
+    dev = _device(rows if x is None else x)
+    stream_side, block_side = r if x is None else x, s if rows is None else rows
+    xt = bt = None
+    xk = bk = 0
+    if stream_side is not None:
+        xt, xk = stream_side.dtype, _type(stream_side)
+    if block_side is not None:
+        bt, bk = block_side.dtype, _type(block_side)
+    ga, gk, g0, g1 = (None, 0, 1, 1) if gate is None else _gate(gate, M, K, dev)
     R = M if expanded_row_idx is None else M * d.top_k
-    stream_side, block_side = _first(x, r), _first(rows, s)
-    xt = None if stream_side is None else stream_side.dtype
-    bt = None if block_side is None else block_side.dtype
-    ga, gk, g0, g1 = _gate(gate, M, K, dev)
-    _launch("megamoe_norm", dev, stream, ctypes.byref(d), _at("x", x, xt, (M, K), dev),
-            0 if xt is None else _type(stream_side), _at("rows", rows, bt, (R, K), dev),
-            0 if bt is None else _type(block_side),
-            _at("expanded_row_idx", expanded_row_idx, torch.int32, (R,), dev),
-            _at("w_after", w_after, f32, (K,), dev), ga, gk, g0, g1, alpha,
-            _at("w_before", w_before, f32, (K,), dev), eps, _at("s", s, bt, (M, K), dev),
-            _at("r", r, xt, (M, K), dev), _at("h", h, None, (M, K), dev),
-            0 if h is None else _type(h))
+    _launch("megamoe_norm", dev, stream, ctypes.byref(d),
+            None if x is None else _at("x", x, xt, (M, K), dev), xk,
+            None if rows is None else _at("rows", rows, bt, (R, K), dev), bk,
+            None if expanded_row_idx is None
+            else _at("expanded_row_idx", expanded_row_idx, torch.int32, (R,), dev),
+            None if w_after is None else _at("w_after", w_after, f32, (K,), dev), ga, gk, g0, g1, alpha,
+            None if w_before is None else _at("w_before", w_before, f32, (K,), dev), eps,
+            None if s is None else _at("s", s, bt, (M, K), dev),
+            None if r is None else _at("r", r, xt, (M, K), dev),
+            None if h is None else _at("h", h, None, (M, K), dev), 0 if h is None else _type(h))
 
 
 def megamoe_norm_grad_workspace_bytes(d: megamoe_dims) -> int:
@@ -214,8 +217,8 @@ def megamoe_route_grad(d, logits, expert_idx, probs, dprobs, dlogits, bias=None,
     M, E, k, dev = d.M, d.E, d.top_k, _device(logits)
     _launch("megamoe_route_grad", dev, stream, ctypes.byref(d),
             _at("logits", logits, None, (M, E), dev), 0 if logits is None else _type(logits),
-            _at("bias", bias, torch.float32, (E,), dev), 1 if renormalize else 0,
-            _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
+            None if bias is None else _at("bias", bias, torch.float32, (E,), dev),
+            1 if renormalize else 0, _at("expert_idx", expert_idx, torch.int32, (M, k), dev),
             _at("probs", probs, torch.float32, (M, k), dev),
             _at("dprobs", dprobs, torch.float32, (M, k), dev),
             _at("dlogits", dlogits, None if logits is None else logits.dtype, (M, E), dev))
