@@ -167,10 +167,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void h
     }
 }
 
-// Measured on both sides, this kernel and the 256-row tiles, in us.  K = 7168, I = 2048, E = 32, with SwiGLU: mean 1 row
-// an expert 181 / 243, 4 rows 289 / 298, 16 rows 304 / 313, 32 rows 312 / 305, 64 rows 466 / 323; without, of 32 rows
-// 345 / 355, of 50 403 / 355; second product: 4 rows 161 / 197, 16 rows 165 / 190, 32 rows 182 / 208, 64 rows 263 / 227.
-// K = 4096, I = 1408, E = 64, Zipf(1.2) routing: 12 rows 261 / 275, 28 rows 277 / 264.
+// Measured on both sides, this kernel and the 256-row tiles, in us, by mean rows an expert.  K = 7168, I = 2048, E = 32:
+// first product 1 row 186 / 246, 4 298 / 309, 16 317 / 318, 32 346 / 355, 40 335 / 333, 64 538 / 331; second product
+// 112 / 130, 155 / 196, 155 / 182, 190 / 233, 185 / 237, 243 / 197.  K = 4096, I = 1408, E = 64, Zipf(1.2) routing: 28
+// rows 304 / 321 and 157 / 168, 38 rows 343 / 316 and 173 / 170.
 bool half_few_ok(const HalfGmmParams &p) { return (p.R + p.E - 1) / p.E <= 36; }
 
 template <int T, bool SWIGLU, int NP>

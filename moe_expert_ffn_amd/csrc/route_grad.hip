@@ -27,6 +27,9 @@ __device__ __forceinline__ float rg_exp(float x, float most) {
 // `lanes` lanes (a power of two) to a token: lane j has its slot j and the experts 8 j + 0..7, so that a row is read and
 // written 16 bytes at a time.  What the slots add to their experts meets the experts in LDS; a slot whose expert an
 // earlier slot names leaves its part to that one, so that the order of the sum is fixed.
+// 32768 tokens of 256 bf16 logits, 8 slots: 37 MB in 12.9 us, 2.9 TB/s.  Instructions bound it, not memory (7.4 us):
+// VALUs are active in 57% of the cycles, the shuffles over the slots among them.  A wave to a token, four experts a lane and
+// each looking through all slots, took 29.7.  128 tokens of 32 fp32 logits: 7.1 us, the call itself.
 template <int T>
 __global__ __launch_bounds__(kRgBlock) void route_grad_kernel(RouteGradParams p, int lanes) {
     __shared__ __align__(16) float s_gain[kRgBlock * 8];
@@ -102,7 +105,8 @@ __global__ __launch_bounds__(kRgBlock) void route_grad_kernel(RouteGradParams p,
     if (mine) Element<T>::store_nt(p.dlogits, t * p.E + 8 * j, y);
 }
 
-// Rows that are not whole pieces of 8, or more than 64 slots: a wave to a token, lane l with the experts l + 64 v.
+// Rows that are not whole pieces of 8, or more than 64 slots, of which no lane has one each: a wave to a token, lane l
+// with the experts l + 64 v.  (32768 tokens of 256 logits: 29.7 us for 12.9.)
 template <int T>
 __global__ __launch_bounds__(64) void route_grad_any_kernel(RouteGradParams p) {
     const size_t t = blockIdx.x;
