@@ -24,22 +24,29 @@ __device__ __forceinline__ float rg_exp(float x, float most) {
     return x == most ? 1.0f : __builtin_amdgcn_exp2f((x - most) * 1.4426950408889634f);
 }
 
-// `lanes` lanes (a power of two) to a token: lane j has its slot j and the experts 8 j + 0..7, so that a row is read and
-// written 16 bytes at a time.  What the slots add to their experts meets the experts in LDS; a slot whose expert an
+// `lanes` lanes (a power of two) to a token: lane j has its slot j and eight experts: with PIECES 8 j + 0..7, so that a row is
+// read and written 16 bytes at a time, else j + lanes v, for rows that are not whole pieces of 8.  What the slots add to their experts meets the experts in LDS; a slot whose expert an
 // earlier slot names leaves its part to that one, so that the order of the sum is fixed.
-// 32768 tokens of 256 bf16 logits, 8 slots: 37 MB in 12.9 us, 2.9 TB/s.  Instructions bound it, not memory (7.4 us):
+// 32768 tokens of 256 bf16 logits, 8 slots: 37 MB in 12.9 us, 2.9 TB/s; of 255 17.4 (a wave to a token: 50).  Instructions bound it, not memory (7.4 us):
 // VALUs are active in 57% of the cycles, the shuffles over the slots among them.  A wave to a token, four experts a lane and
 // each looking through all slots, took 29.7.  128 tokens of 32 fp32 logits: 7.1 us, the call itself.
-template <int T>
+template <int T, bool PIECES>
 __global__ __launch_bounds__(kRgBlock) void route_grad_kernel(RouteGradParams p, int lanes) {
     __shared__ __align__(16) float s_gain[kRgBlock * 8];
     const int tid = threadIdx.x, j = tid & (lanes - 1), group = tid / lanes;
     const size_t t = (size_t)blockIdx.x * (kRgBlock / lanes) + group;
-    const bool here = t < (size_t)p.M, mine = here && 8 * j < p.E;
+    const bool here = t < (size_t)p.M, mine = here && (PIECES ? 8 * j : j) < p.E;
     float *gain = s_gain + group * lanes * 8;
     float x[8];
     typename Element<T>::Raw raw;
-    if (mine && !p.renormalize) raw = Element<T>::load_nt(p.logits, t * p.E + 8 * j);
+    if (mine && !p.renormalize) {
+        if constexpr (PIECES) {
+            raw = Element<T>::load_nt(p.logits, t * p.E + 8 * j);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) x[v] = Element<T>::load1(p.logits, t * p.E + min(j + lanes * v, p.E - 1));
+        }
+    }
     int id = -1;
     float w = 0.0f, g = 0.0f;
     if (here && j < p.top_k) {
@@ -69,22 +76,33 @@ __global__ __launch_bounds__(kRgBlock) void route_grad_kernel(RouteGradParams p,
     if (first) gain[id] = total;
     __syncthreads();
     float y[8];
+    if constexpr (PIECES) {
 #pragma unroll
-    for (int v = 0; v < 8; v += 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(gain + 8 * j + v);
-        y[v] = q.x;
-        y[v + 1] = q.y;
-        y[v + 2] = q.z;
-        y[v + 3] = q.w;
+        for (int v = 0; v < 8; v += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(gain + 8 * j + v);
+            y[v] = q.x;
+            y[v + 1] = q.y;
+            y[v + 2] = q.z;
+            y[v + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v) y[v] = gain[j + lanes * v];
     }
     if (!p.renormalize) {
         float most = -INFINITY, sum = 0.0f;
         if (mine) {
             float b[8] = {};
-            Element<T>::values(raw, x);
-            if (p.bias) Element<kFp32>::values(Element<kFp32>::load(p.bias, 8 * j), b);
+            if constexpr (PIECES) {
+                Element<T>::values(raw, x);
+                if (p.bias) Element<kFp32>::values(Element<kFp32>::load(p.bias, 8 * j), b);
+            } else if (p.bias) {
 #pragma unroll
-            for (int v = 0; v < 8; ++v) x[v] = rg_part(x[v], b[v]);
+                for (int v = 0; v < 8; ++v) b[v] = p.bias[min(j + lanes * v, p.E - 1)];
+            }
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                x[v] = PIECES || j + lanes * v < p.E ? rg_part(x[v], b[v]) : -INFINITY;
         } else {
 #pragma unroll
             for (int v = 0; v < 8; ++v) x[v] = -INFINITY;
@@ -102,11 +120,18 @@ __global__ __launch_bounds__(kRgBlock) void route_grad_kernel(RouteGradParams p,
 #pragma unroll
         for (int v = 0; v < 8; ++v) y[v] = x[v] == 0.0f ? 0.0f : x[v] * inv * (y[v] - dot);
     }
-    if (mine) Element<T>::store_nt(p.dlogits, t * p.E + 8 * j, y);
+    if (!mine) return;
+    if constexpr (PIECES) {
+        Element<T>::store_nt(p.dlogits, t * p.E + 8 * j, y);
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            if (j + lanes * v < p.E) Element<T>::store1(p.dlogits, t * p.E + j + lanes * v, y[v]);
+    }
 }
 
-// Rows that are not whole pieces of 8, or more than 64 slots, of which no lane has one each: a wave to a token, lane l
-// with the experts l + 64 v.  (32768 tokens of 256 logits: 29.7 us for 12.9.)
+// More than 64 slots, of which no lane has one each: a wave to a token, lane l with the experts l + 64 v, all of them
+// looking through all slots.
 template <int T>
 __global__ __launch_bounds__(64) void route_grad_any_kernel(RouteGradParams p) {
     const size_t t = blockIdx.x;
@@ -148,14 +173,15 @@ __global__ __launch_bounds__(64) void route_grad_any_kernel(RouteGradParams p) {
 
 template <int T>
 static void rg_launch(const RouteGradParams &p, hipStream_t stream) {
-    if (p.E % 8 != 0 || p.top_k > kWave) {
+    if (p.top_k > kWave) {
         hipLaunchKernelGGL(route_grad_any_kernel<T>, dim3(p.M), dim3(64), 0, stream, p);
         return;
     }
     int lanes = 1;
     while (8 * lanes < p.E || lanes < p.top_k) lanes *= 2;
     const int tokens = kRgBlock / lanes;
-    hipLaunchKernelGGL(route_grad_kernel<T>, dim3((p.M + tokens - 1) / tokens), dim3(kRgBlock), 0, stream, p, lanes);
+    hipLaunchKernelGGL((p.E % 8 == 0 ? route_grad_kernel<T, true> : route_grad_kernel<T, false>),
+                       dim3((p.M + tokens - 1) / tokens), dim3(kRgBlock), 0, stream, p, lanes);
 }
 
 hipError_t launch_route_grad(const RouteGradParams &p, int type, hipStream_t stream) {

@@ -1,0 +1,51 @@
+"""What the smaller problems of test_gpu_half.py and test_gpu_norm.py do not reach: workgroups that look up their tiles several
+times, and that go on to further tokens at every width."""
+from __future__ import annotations
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from moe_expert_ffn_amd import half as H  # noqa: E402
+from tests import half64 as P  # noqa: E402
+from tests import test_gpu_half as G  # noqa: E402
+from tests import test_gpu_norm as N  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+_gpu = G._gpu
+
+
+@pytest.mark.parametrize("counts", [[9000, 0, 31, 7900, 300], [6000, 6001, 5200]])
+def test_products_of_many_tiles(counts):
+    """More than 32 tiles to each of 256 workgroups, of every size, an incomplete last round among them."""
+    c = G.Case(sum(counts), 128, len(counts), 1, 16384, G.counted(counts), torch.bfloat16)
+    assert sum((n + 255) // 256 for n in counts) * 128 > 32 * 256
+    out, y = c.out(2 * c.I), c.out(c.I)
+    H.megamoe_half_gmm1(c.d, c.x, c.route, c.end, c.w1, out)
+    H.megamoe_half_gmm1_swiglu(c.d, c.x, c.route, c.end, c.w1, y, probs=c.probs)
+    v, b = P.product(c.x, c.token, c.w1, c.end, c.R)
+    for i in range(0, c.R, 1000):
+        near = slice(i, i + 1000)
+        G.near("gmm1", out[near], v[near], b[near], c.t)
+        w, e = P.swiglu(v[near], c.p[near], b[near])
+        G.near("gmm1_swiglu", y[near], w, e, c.t)
+    del v, b, out, y
+    # as many tiles the other way: the weights' gradient, all of whose rows are there
+    dw = torch.full((c.E, 2 * c.I, c.K), math.nan, dtype=c.t, device="cuda")
+    H.megamoe_half_gmm1_wgrad(c.d, c.dc, c.x, c.route, c.end, dw)
+    v, b = P.weights(c.dc, None, c.x, c.token, c.end, c.E)
+    G.near("gmm1_wgrad", dw, v, b, c.t)
+
+
+@pytest.mark.parametrize("M,K,x,rows,h,k,after,gate,with_dr,before", [
+    (600, 7168, "bf16", "bf16", "bf16", 3, True, "channel", True, True),
+    (530, 8192, "fp32", "fp16", "bf16", 0, True, "token", True, True),
+    (300, 12288, "bf16", "bf16", "bf16", 2, True, "channel", True, True),
+    (1500, 4096, "fp32", "bf16", "bf16", 2, True, "one", True, True),
+    (2200, 2048, "fp16", "fp16", "fp16", 2, True, "channel", True, True),
+    (2100, 512, "bf16", "bf16", "fp32", 1, True, "element", False, True),
+])
+def test_norm_gradients_over_several_tokens(M, K, x, rows, h, k, after, gate, with_dr, before):
+    N.test_norm_gradients(M, K, x, rows, h, k, after, gate, with_dr, before)

@@ -213,7 +213,7 @@ def test_norm_gradients(M, K, x, rows, h, k, after, gate, with_dr, before):
             mag = mag + e + rh * (e * rh).mean(1, keepdim=True)
         bound = {"dx": mag * rel}
         if before:
-            # tokens in a row: at most M / 512 + 1 in a workgroup and 512 / 4 + 4 parts
+            # tokens in a row: at most M / 256 + 1 in a workgroup, and 1024 / 16 + 16 parts; M <= 2200 here
             bound["dw_before"] = (dha * rh).sum(0) * (rel + (M / 512 + 140) * P.U)
         if rows:
             ss = 1 / torch.sqrt(S.double().square().mean(1, keepdim=True) + EPS) if after else 1.0
