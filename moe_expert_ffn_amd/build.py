@@ -121,7 +121,7 @@ def check_half_resources(remarks: str) -> list[str]:
     problems = []
     found = 0
     for name, r in kernel_resources(remarks).items():
-        if "half_gmm_kernel" not in name and "half_few_kernel" not in name:
+        if not re.search("half_(gmm|few|small)_kernel", name):
             continue
         found += 1
         spills, scratch = r.get("VGPRs Spill", 0), r.get("ScratchSize", 0)

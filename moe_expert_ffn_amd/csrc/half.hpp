@@ -24,6 +24,9 @@ struct HalfGmmParams {
 // ... of few rows an expert (half_few.hip)
 bool half_few_ok(const HalfGmmParams &p);
 hipError_t launch_half_few(const HalfGmmParams &p, int type, hipStream_t stream);
+// ... of few tiles (half_small.hip)
+bool half_small_ok(const HalfGmmParams &p, int kind, int cu_count);
+hipError_t launch_half_small(const HalfGmmParams &p, int kind, int type, hipStream_t stream);
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream);
 
 // SwiGLU of 16-bit rows and its gradient (half_swiglu.hip).

@@ -23,49 +23,6 @@ __device__ __forceinline__ v16f few_mfma(v4i w, v4i a, v16f acc) {
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, a), acc, 0, 0, 0);
 }
-__device__ __forceinline__ int few_swz(int row, int c) { return c ^ (row >> 1 & 7); }
-
-struct FewTile {
-    int e, row0, rows, nblk;
-};
-struct FewSchedule {
-    int w[4], pre[kHgE + 1], first[kHgE], rows[kHgE];
-};
-
-// Tiles by expert, weight block and row block; -1 for e where there are not so many.
-template <int RB>
-__device__ __forceinline__ FewTile few_find_tile(const HalfGmmParams &p, int t, int cols, FewSchedule &s) {
-    const int e = threadIdx.x, lane = e & (kWave - 1), wave = e >> 6;
-    const int first = e < p.E ? hg_row_end(p, e - 1) : 0;
-    const int rows = e < p.E ? max(0, hg_row_end(p, e) - first) : 0;
-    const int nb = (p.N + cols - 1) / cols, tiles = (rows + RB - 1) / RB * nb;
-    const int incl = wave_inclusive_scan(tiles);
-    if (lane == kWave - 1) s.w[wave] = incl;
-    s.first[e] = first;
-    s.rows[e] = rows;
-    __syncthreads();
-    int pre = incl - tiles;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) pre += w < wave ? s.w[w] : 0;
-    s.pre[e] = pre;
-    if (e == kHgE - 1) s.pre[kHgE] = pre + tiles;
-    __syncthreads();
-    const int total = __builtin_amdgcn_readfirstlane(s.pre[kHgE]);
-    // workgroups go round the XCDs: each XCD takes a run of neighbouring tiles, which share weights or rows
-    const int per = (total + 7) / 8;
-    t = (t & 7) * per + (t >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || t >= total) return FewTile{-1, 0, 0, 0};
-    int lo = 0, hi = kHgE - 1;  // the first expert that ends after t
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s.pre[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    const int n = s.rows[lo], local = t - s.pre[lo], mb = (n + RB - 1) / RB, m = local % mb;
-    return FewTile{__builtin_amdgcn_readfirstlane(lo), __builtin_amdgcn_readfirstlane(s.first[lo] + m * RB),
-                   __builtin_amdgcn_readfirstlane(min(RB, n - m * RB)), __builtin_amdgcn_readfirstlane(local / mb)};
-}
-
 template <int T, bool SWIGLU, int NP>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void half_few_kernel(HalfGmmParams p) {
     constexpr int RB = 32 * NP, COLS = SWIGLU ? kFewRows / 2 : kFewRows, SLOT = (RB + kFewRows) * 128;
@@ -93,7 +50,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void h
         // with SwiGLU a wave's 32 are 16 for silu and the 16 of the gate that go with them
         const int r = (wave * 4 + i) * 8 + (lane >> 3), in = r & 31;
         const int col = t.nblk * COLS + (SWIGLU ? 16 * wave + (in & 15) : r);
-        vw[i] = (uint32_t)(min(col, p.N - 1) + (SWIGLU && in >= 16 ? p.N : 0)) * ld + few_swz(r, lane & 7) * 16;
+        vw[i] = (uint32_t)(min(col, p.N - 1) + (SWIGLU && in >= 16 ? p.N : 0)) * ld + hg_swz(r, lane & 7) * 16;
     }
     auto issue_w = [&](int s) {
         const uint32_t to = at + s % SLOTS * SLOT + RB * 128 + wave * 4096;
@@ -109,7 +66,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void h
 #pragma unroll
     for (int i = 0; i < NP; ++i)
         va[i] = (p.gather ? hg_token(p, route[i]) : (uint32_t)route[i]) * ld +
-                few_swz((wave * NP + i) * 8 + (lane >> 3), lane & 7) * 16;
+                hg_swz((wave * NP + i) * 8 + (lane >> 3), lane & 7) * 16;
 #pragma unroll
     for (int s = 0; s < SLOTS - 1; ++s)
         if (s < ns) {
@@ -131,7 +88,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void h
         const uint8_t *q = s_data + s % SLOTS * SLOT + r * 128;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            const int place = few_swz(r, 2 * h + g) * 16;
+            const int place = hg_swz(r, 2 * h + g) * 16;
             const v4i wf = *reinterpret_cast<const v4i *>(q + RB * 128 + wave * 4096 + place);
 #pragma unroll
             for (int i = 0; i < NP; ++i)

@@ -15,21 +15,6 @@
 
 namespace megamoe {
 
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-
-// 16 x 16 x 32 with the columns' operand first: lane l holds output row l & 15 and the columns 4 (l >> 4) + 0..3.  Of
-// either operand lane l has row l & 15 and 8 (l >> 4) + 0..7 of the reduction.  (From registers, on random operands,
-// for which the card lowers its clock, it ran at 2030 TFLOP/s and the 32 x 32 x 16 form at 1730, as that one
-// goes through its sums twice as often; on zeros 2420 and 2470.)
-template <int T>
-__device__ __forceinline__ v4f hg_mfma(v4i w, v4i a, v4f acc) {
-    if constexpr (T == kBf16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w), __builtin_bit_cast(v8bf, a), acc, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, w), __builtin_bit_cast(v8h, a), acc, 0, 0, 0);
-}
-
 // ---------------------------------------------------------------------------
 // Tiles of 256 rows by 256 columns, four waves to a tile and one to a SIMD, each multiplying all of
 // its rows by 64 of its columns: 16 x 4 fragments of 16 x 16 sums fill half of the register file, and the time of a
@@ -175,10 +160,6 @@ struct HgLds {
     uint32_t route_at, weight_at;
 };
 
-// 16-byte piece c of a row that lies along the reduction: its place.  LDS has 64 banks, two rows; reads of one
-// piece of 16 rows in the order of the lanes meet each bank once.
-__device__ __forceinline__ int hg_swz(int row, int c) { return c ^ (row >> 1 & 7); }
-
 // One 16-byte piece a lane into LDS through a buffer: 0 where voff is not within it.
 __device__ __forceinline__ void dma16_buffer(v4i rsrc, uint32_t voff, uint32_t lds_base) {
     asm volatile(
@@ -302,39 +283,6 @@ __device__ __forceinline__ void hg_all(const I &issue) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) issue.copy(i);
 }
-
-// Fragments of an operand in LDS.
-template <bool ACROSS>
-struct HgRead {
-    const uint8_t *at;
-    int place[4];  // along: of the lane's piece of each step of 32, two; across: of the quarters of a panel
-    __device__ __forceinline__ HgRead() {}
-    __device__ __forceinline__ void lane_places() {
-        const int lane = threadIdx.x & 63;
-        if constexpr (ACROSS) {
-            // row 8 (lane >> 4) + ((lane & 15) >> 2), and four on; columns 4 (lane & 3) + 0..3
-            const int in = (lane >> 4) * 1024 + ((lane & 15) >> 2) * 128 + (lane & 3) * 8;
-            const int swap = (lane >> 3 & 1) * 2 + (lane >> 4 & 1);  // bits 1 and 3 of the row
-#pragma unroll
-            for (int q = 0; q < 4; ++q) place[q] = in + (q ^ swap) * 32;
-        } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) place[h] = (lane & 15) * 128 + hg_swz(lane & 15, 4 * h + (lane >> 4)) * 16;
-        }
-    }
-    // fragment f of 16 rows or columns, step h
-    __device__ __forceinline__ void read(int f, int h, v4i &v) const {
-        if constexpr (ACROSS) {
-            typedef __attribute__((address_space(3))) v4s *P;
-            const uint8_t *q = at + place[f & 3] + (f >> 2) * 8192 + h * 4096;
-            const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)q));
-            const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(q + 512)));
-            v = v4i{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
-        } else {
-            v = *reinterpret_cast<const v4i *>(at + f * 2048 + place[h]);
-        }
-    }
-};
 
 // One sum out of the accumulation registers.  (Left to the compiler, all 256 are copied
 // at once and other values spill.)
@@ -746,6 +694,7 @@ static void hg_launch(const HalfGmmParams &p, int cu_count, hipStream_t stream) 
 
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream) {
     const bool b = type == kBf16;
+    if (kind != kHalfWeights && half_small_ok(p, kind, cu_count)) return launch_half_small(p, kind, type, stream);
     if (kind == kHalfProduct && half_few_ok(p)) return launch_half_few(p, type, stream);
     if (kind == kHalfProduct && p.swiglu) {
         if (b) hg_launch<HgGeom<kHalfProduct, kBf16, true>>(p, cu_count, stream);
