@@ -694,7 +694,7 @@ static void hg_launch(const HalfGmmParams &p, int cu_count, hipStream_t stream) 
 
 hipError_t launch_half_gmm(const HalfGmmParams &p, int kind, int type, int cu_count, hipStream_t stream) {
     const bool b = type == kBf16;
-    if (kind != kHalfWeights && half_small_ok(p, kind, cu_count)) return launch_half_small(p, kind, type, stream);
+    if (half_small_ok(p, kind, cu_count)) return launch_half_small(p, kind, type, stream);
     if (kind == kHalfProduct && half_few_ok(p)) return launch_half_few(p, type, stream);
     if (kind == kHalfProduct && p.swiglu) {
         if (b) hg_launch<HgGeom<kHalfProduct, kBf16, true>>(p, cu_count, stream);
