@@ -49,3 +49,43 @@ def test_products_of_many_tiles(counts):
 ])
 def test_norm_gradients_over_several_tokens(M, K, x, rows, h, k, after, gate, with_dr, before):
     N.test_norm_gradients(M, K, x, rows, h, k, after, gate, with_dr, before)
+
+
+EDGES = [[63, 64, 65], [0, 0, 127, 128, 129, 0], [191, 192, 193], [255, 256, 257], [511, 512, 513, 0], [40, 1, 300, 31, 33]]
+
+
+def _wide(K, I):
+    for t in ("bf16", "fp16"):
+        for c in EDGES:
+            yield pytest.param(lambda c=c, t=t: G.Case(sum(c), K, len(c), 1, I, G.counted(c), G.T[t]),
+                               id=f"{t}-K{K}-I{I}-rows-" + "-".join(map(str, c)))
+        for how in ("drop", "zipf", "one", "none", "twice"):
+            yield pytest.param(lambda how=how, t=t: G.Case(130, K, 5, 2, I, G.make_ids(130, 5, 2, how, 7), G.T[t]),
+                               id=f"{t}-K{K}-I{I}-{how}")
+
+
+# so wide that few rows make many tiles, and the other way about: each product meets the kernel of many tiles in one of them
+WIDE = list(_wide(256, 8192)) + list(_wide(8192, 256))
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_wide_products(case):
+    G.test_products(case)
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_wide_row_gradients(case):
+    G.test_row_gradients(case)
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_wide_weight_gradients(case):
+    G.test_weight_gradients(case)
+
+
+@pytest.mark.parametrize("t", sorted(G.T))
+@pytest.mark.parametrize("M,K,I", [(200, 256, 8192), (200, 8192, 256), (40, 2048, 256)])
+def test_nothing_leaks_between_wide_groups(M, K, I, t, monkeypatch):
+    case = G.Case
+    monkeypatch.setattr(G, "Case", lambda m, k, E, top_k, i, ids, kind: case(M, K, E, top_k, I, ids[:M].contiguous(), kind))
+    G.test_nothing_leaks_between_groups(t)
