@@ -1,4 +1,4 @@
-// What the two kernels of the 16-bit products share.
+// What the kernels of the 16-bit products share.
 #pragma once
 
 #include "common.hpp"
