@@ -484,8 +484,46 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
     const int r = lane & 15, g = lane >> 4;
     const int n0 = t.nblk * G::COLS + wave * 16 * J;
     const size_t out_row = G::WEIGHTS ? (size_t)t.e * p.M + t.row0 : (size_t)t.row0;
-    if (G::WEIGHTS && (p.accumulate || p.c_type == kFp32)) {
-        // four columns a lane, in fp32 or added to what is there
+    const bool low = r < 8;
+    // Lanes l and l ^ 8 exchange four words: of two pieces of a row, x and y, in lines one after the other, each lane
+    // then has one of row r & 7 in x and one of row 8 + (r & 7) in y, so that a store has the whole lines of eight rows.
+    auto exchange = [&](v4i &x, v4i &y) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int keep = low ? x[v] : y[v], give = low ? y[v] : x[v];
+            const int got = __builtin_amdgcn_update_dpp(0, give, 0x128, 0xf, 0xf, false);  // of lane l ^ 8
+            x[v] = low ? keep : got;
+            y[v] = low ? got : keep;
+        }
+    };
+    if (G::WEIGHTS && p.c_type == kFp32) {
+        // four columns a lane; stored as the 16-bit weights below (64 groups of 384 rows, 4096 x 1408: 517 us for 572)
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) {
+#pragma unroll
+            for (int j = 0; j < J; j += 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                v4i q[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) q[h][v] = __float_as_int(hg_sum(acc[i][j + h][v]));
+                exchange(q[0], q[1]);
+                const int col = n0 + 16 * (j + (r >> 3)) + 4 * g;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = 16 * i + 8 * h + (r & 7);
+                    if (row >= t.rows || col >= p.N) continue;
+                    v4f *o = reinterpret_cast<v4f *>((float *)p.c + (out_row + row) * p.N + col);
+                    v4f y = __builtin_bit_cast(v4f, q[h]);
+                    if (p.accumulate) y += *o;
+                    __builtin_nontemporal_store(y, o);
+                }
+            }
+        }
+        return;
+    }
+    if (G::WEIGHTS && p.accumulate) {  // four columns a lane, added to what is there
 #pragma unroll
         for (int i = 0; i < 2 * NP; ++i) {
             __builtin_amdgcn_sched_barrier(0);
@@ -497,19 +535,11 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
                 for (int v = 0; v < 4; ++v) y[v] = hg_sum(acc[i][j][v]);
                 const int col = n0 + 16 * j + 4 * g;
                 if (row >= t.rows || col >= p.N) continue;
-                const size_t at = (out_row + row) * p.N + col;
-                if (p.c_type == kFp32) {
-                    float4 *o = reinterpret_cast<float4 *>((float *)p.c + at);
-                    float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (p.accumulate) old = *o;
-                    *o = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
-                } else {
-                    uint2 *o = reinterpret_cast<uint2 *>((uint16_t *)p.c + at);
-                    const uint2 old = *o;
-                    typedef Element<T> L;
-                    *o = make_uint2(L::pack(L::lo(old.x) + y[0], L::hi(old.x) + y[1]),
-                                    L::pack(L::lo(old.y) + y[2], L::hi(old.y) + y[3]));
-                }
+                uint2 *o = reinterpret_cast<uint2 *>((uint16_t *)p.c + (out_row + row) * p.N + col);
+                const uint2 old = *o;
+                typedef Element<T> L;
+                *o = make_uint2(L::pack(L::lo(old.x) + y[0], L::hi(old.x) + y[1]),
+                                L::pack(L::lo(old.y) + y[2], L::hi(old.y) + y[3]));
             }
         }
         return;
@@ -549,16 +579,7 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
                 const auto y = __builtin_amdgcn_permlane16_swap(out[i][j].y, out[i][j + 1].y, false, false);
                 q[j / 2] = v4i{(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
             }
-            const bool low = r < 8;
-            if constexpr (G::WEIGHTS) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int keep = low ? q[0][v] : q[1][v], give = low ? q[1][v] : q[0][v];
-                    const int got = __builtin_amdgcn_update_dpp(0, give, 0x128, 0xf, 0xf, false);  // of lane l ^ 8
-                    q[0][v] = low ? keep : got;
-                    q[1][v] = low ? got : keep;
-                }
-            }
+            if constexpr (G::WEIGHTS) exchange(q[0], q[1]);
 #pragma unroll
             for (int j = 0; j < J / 2; ++j) {
                 const int row = 64 * pair + 16 * i + (G::WEIGHTS ? 8 * j + (r & 7) : r);
