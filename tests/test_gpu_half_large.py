@@ -89,3 +89,43 @@ def test_nothing_leaks_between_wide_groups(M, K, I, t, monkeypatch):
     case = G.Case
     monkeypatch.setattr(G, "Case", lambda m, k, E, top_k, i, ids, kind: case(M, K, E, top_k, I, ids[:M].contiguous(), kind))
     G.test_nothing_leaks_between_groups(t)
+
+
+@pytest.mark.parametrize("M", [70, 200])
+def test_largest_widths(M):
+    """K and I at their limits: an expert's weights are 2^31 bytes."""
+    case = G.Case(M, 32768, 2, 1, 16384, G.counted([M // 2 - 3, M - M // 2 + 3]), torch.bfloat16)
+    G.test_products(lambda: case)
+    torch.cuda.empty_cache()
+    G.test_row_gradients(lambda: case)
+    torch.cuda.empty_cache()
+    # the weights' gradient, whole rows of it: an expert's in 64 bits would be 8 GiB each for values and bounds
+    dw = torch.full((2, 2 * case.I, case.K), math.nan, dtype=case.t, device="cuda")
+    H.megamoe_half_gmm1_wgrad(case.d, case.dc, case.x, case.route, case.end, dw)
+    assert torch.isfinite(dw).all()
+    for rows in (slice(0, 300), slice(16300, 16500), slice(32468, 32768)):
+        v, b = P.weights(case.dc[:, rows], None, case.x, case.token, case.end, 2)
+        G.near("gmm1_wgrad", dw[:, rows], v, b, case.t)
+
+
+def test_rows_of_nearly_2_to_32_bytes():
+    case = G.Case(65000, 32768, 5, 1, 128, G.counted([20000, 3, 0, 24997, 20000]), torch.bfloat16)
+    assert 0.98 * 2 ** 31 < case.R * case.K < 2 ** 31
+    out = case.out(2 * case.I)
+    H.megamoe_half_gmm1(case.d, case.x, case.route, case.end, case.w1, out)
+    v, b = P.product(case.x, case.token, case.w1, case.end, case.R)
+    G.near("gmm1", out, v, b, case.t)
+    dw = torch.full((5, 2 * case.I, case.K), math.nan, dtype=case.t, device="cuda")
+    H.megamoe_half_gmm1_wgrad(case.d, case.dc, case.x, case.route, case.end, dw)
+    v, b = P.weights(case.dc, None, case.x, case.token, case.end, 5)
+    G.near("gmm1_wgrad", dw, v, b, case.t)
+    dy = case.out(case.I)
+    H.megamoe_half_gmm2_dgrad(case.d, case.dout, case.route, case.end, case.w2, dy)
+    v, b = P.product(case.dout, case.token, case.w2, case.end, case.R, transposed=True)
+    G.near("gmm2_dgrad", dy, v, b, case.t)
+    dx = case.out(case.K)
+    H.megamoe_half_gmm1_dgrad(case.d, case.dc, case.end, case.w1, dx)
+    for lo, hi in ((0, 300), (19990, 20010), (44900, 45100), (64700, 65000)):
+        end = (case.end - lo).clamp(0, hi - lo)
+        v, b = P.product(case.dc[lo:hi], None, case.w1, end, hi - lo, transposed=True)
+        G.near("gmm1_dgrad", dx[lo:hi], v, b, case.t)
