@@ -116,12 +116,16 @@ def check_gemm_resources(remarks: str) -> list[str]:
     return problems
 
 
+# the kernels of the 16-bit products; each has to be in the report, under this name
+HALF_KERNELS = ("half_gmm_kernel", "half_few_kernel", "half_small_kernel", "half_small_weights_kernel")
+
+
 def check_half_resources(remarks: str) -> list[str]:
     """No instantiation of the 16-bit products spills a vector value."""
     problems = []
     found = 0
     for name, r in kernel_resources(remarks).items():
-        if not re.search("half_(gmm|few|small)_kernel", name):
+        if not any(k in name for k in HALF_KERNELS):
             continue
         found += 1
         spills, scratch = r.get("VGPRs Spill", 0), r.get("ScratchSize", 0)
@@ -129,6 +133,19 @@ def check_half_resources(remarks: str) -> list[str]:
             problems.append(f"16-bit product {name}: vector spills {spills}, scratch {scratch} bytes a lane")
     if not found:
         problems.append("no 16-bit product found in the resource report")
+    return problems
+
+
+def check_half_kernels(remarks: str, srcs: list[str]) -> list[str]:
+    """The kernels that check_half_resources looks at are those of the products' sources, and all are reported."""
+    names = list(kernel_resources(remarks))
+    problems = [f"16-bit product {k}: not in the resource report" for k in HALF_KERNELS
+                if not any(k in name for name in names)]
+    for src in srcs:
+        with open(src) as f:
+            declared = re.findall(r"__global__[^;{]*?\b(\w+)\(HalfGmmParams", f.read())
+        problems += [f"16-bit product {k}: not among the kernels that are checked" for k in declared
+                     if k not in HALF_KERNELS]
     return problems
 
 
@@ -202,7 +219,8 @@ def build(verbose: bool = False) -> str:
     remarks = "\n".join(r for _, r in done)
     with open(os.path.join(BUILD, "resource_usage.txt"), "w") as f:
         f.write(remarks)
-    problems = check_gemm_resources(remarks) + check_half_resources(remarks) + check_gemm_loops(gemm_asm)
+    problems = (check_gemm_resources(remarks) + check_half_resources(remarks) + check_half_kernels(remarks, srcs)
+                + check_gemm_loops(gemm_asm))
     if problems:
         raise RuntimeError("GEMM register guard failed:\n  " + "\n  ".join(problems))
     tmp = LIB + f".tmp{os.getpid()}"
