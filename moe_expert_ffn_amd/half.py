@@ -11,8 +11,8 @@ from typing import NamedTuple
 
 import torch
 
-from .megamoe import (_at, _check, _device, _launch, _route, _type, dims, load, megamoe_check_dims, megamoe_dims,
-                      megamoe_last_error)
+from .megamoe import (_at, _check, _device, _launch, _route, _type, _workspace, dims, load, megamoe_check_dims,
+                      megamoe_dims, megamoe_last_error)
 
 EXPORTED = [
     "megamoe_sort_routes", "megamoe_half_gmm1", "megamoe_half_gmm1_swiglu", "megamoe_half_gmm2",
@@ -266,8 +266,7 @@ class MegaMoEHalf:
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError(f"expected torch.float16 or torch.bfloat16, got {dtype}")
         self.dtype, self.device = dtype, torch.device(device)
-        self.workspace = torch.empty(megamoe_half_workspace_bytes(self.d), dtype=torch.uint8,
-                                     device=self.device)
+        self.workspace = _workspace(megamoe_half_workspace_bytes(self.d), self.device)
         self.w1 = self.w2 = None
 
     def _empty(self, *shape, dtype=None):
@@ -334,5 +333,5 @@ class MegaMoEHalf:
         return dx_rows, dprobs, dw1, dw2
 
     def last_error(self) -> int:
-        """Routes that the last forward or forward_rows dropped."""
+        """Routes that the last forward or forward_rows dropped, 0 before the first."""
         return megamoe_last_error(self.workspace)

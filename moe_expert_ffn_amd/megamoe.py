@@ -530,6 +530,13 @@ def megamoe_set_overlap(mode: int) -> None:
     _check("megamoe_set_overlap", load().megamoe_set_overlap(int(mode)))
 
 
+def _workspace(n: int, device) -> torch.Tensor:
+    """n bytes, of which the word that last_error reads is 0 until the first forward writes it."""
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:4].zero_()
+    return ws
+
+
 class MegaMoE:
     """Convenience holder: packed weights + workspace for one set of dims.  forward and
     forward_few share the workspace: calls of one holder belong in one order."""
@@ -538,8 +545,7 @@ class MegaMoE:
         self.d = dims(M, K, E, top_k, I)
         _check("megamoe_check_dims", megamoe_check_dims(self.d))
         self.device = torch.device(device)
-        self.workspace = torch.empty(megamoe_workspace_bytes(self.d), dtype=torch.uint8,
-                                     device=self.device)
+        self.workspace = _workspace(megamoe_workspace_bytes(self.d), self.device)
         # forward_few, where the dims allow it, works in the same memory (it needs less), so that
         # the dropped-route word is that of the newest forward on the GPU, replayed graphs included
         self.few_workspace = self.workspace if M <= 16 and M * top_k <= 512 else None
@@ -577,7 +583,7 @@ class MegaMoE:
         return out
 
     def last_error(self) -> int:
-        """Routes that the last forward dropped."""
+        """Routes that the last forward dropped, 0 before the first."""
         return megamoe_last_error(self.workspace)
 
 
@@ -592,7 +598,7 @@ class MegaMoEMXFP4:
         def empty(*shape):
             return torch.empty(shape, dtype=torch.uint8, device=self.device)
 
-        self.workspace = empty(megamoe_mxfp4_workspace_bytes(self.d))
+        self.workspace = _workspace(megamoe_mxfp4_workspace_bytes(self.d), self.device)
         self.w1q, self.w1s = empty(E, 2 * I, K // 2), empty(E, 2 * I, K // 32)
         self.w2q, self.w2s = empty(E, K, I // 2), empty(E, K, I // 32)
         for s in (self.w1s, self.w2s):
@@ -624,7 +630,7 @@ class MegaMoEMXFP4:
         return out
 
     def last_error(self) -> int:
-        """Routes that the last forward dropped."""
+        """Routes that the last forward dropped, 0 before the first."""
         return megamoe_last_error(self.workspace)
 
 
