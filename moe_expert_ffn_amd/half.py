@@ -265,8 +265,9 @@ class MegaMoEHalf:
         _check("megamoe_check_dims", megamoe_check_dims(self.d))
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError(f"expected torch.float16 or torch.bfloat16, got {dtype}")
-        self.dtype, self.device = dtype, torch.device(device)
-        self.workspace = _workspace(megamoe_half_workspace_bytes(self.d), self.device)
+        self.dtype = dtype
+        self.workspace = _workspace(megamoe_half_workspace_bytes(self.d), device)
+        self.device = self.workspace.device  # with its index: "cuda" is another one when another is current
         self.w1 = self.w2 = None
 
     def _empty(self, *shape, dtype=None):

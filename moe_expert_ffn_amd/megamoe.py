@@ -544,8 +544,8 @@ class MegaMoE:
     def __init__(self, M: int, K: int, E: int, top_k: int, I: int, device="cuda"):
         self.d = dims(M, K, E, top_k, I)
         _check("megamoe_check_dims", megamoe_check_dims(self.d))
-        self.device = torch.device(device)
-        self.workspace = _workspace(megamoe_workspace_bytes(self.d), self.device)
+        self.workspace = _workspace(megamoe_workspace_bytes(self.d), device)
+        self.device = self.workspace.device  # with its index: "cuda" is another one when another is current
         # forward_few, where the dims allow it, works in the same memory (it needs less), so that
         # the dropped-route word is that of the newest forward on the GPU, replayed graphs included
         self.few_workspace = self.workspace if M <= 16 and M * top_k <= 512 else None
@@ -593,12 +593,12 @@ class MegaMoEMXFP4:
     def __init__(self, M: int, K: int, E: int, top_k: int, I: int, device="cuda"):
         self.d = dims(M, K, E, top_k, I)
         _check("megamoe_check_dims", megamoe_check_dims(self.d))
-        self.device = torch.device(device)
+        self.workspace = _workspace(megamoe_mxfp4_workspace_bytes(self.d), device)
+        self.device = self.workspace.device  # with its index
 
         def empty(*shape):
             return torch.empty(shape, dtype=torch.uint8, device=self.device)
 
-        self.workspace = _workspace(megamoe_mxfp4_workspace_bytes(self.d), self.device)
         self.w1q, self.w1s = empty(E, 2 * I, K // 2), empty(E, 2 * I, K // 32)
         self.w2q, self.w2s = empty(E, K, I // 2), empty(E, K, I // 32)
         for s in (self.w1s, self.w2s):
