@@ -6,7 +6,9 @@
 // multiplied; two workgroups fit a CU, so that one copies while the other starts or ends.  The code is short: a workgroup goes through
 // it once, and every instruction comes from memory again, as the weights have driven it out of the caches.
 // K = 7168, I = 2048, E = 32, top_k = 8, one token: first product with SwiGLU 70 us, 6.7 TB/s of weights (the 256-row
-// tiles 113; weights straight into registers, half lines at a time, 114), second product 47.
+// tiles 114; weights straight into registers, half lines at a time, 114), second product 37 to 40 (the tiles 47).
+// A workgroup goes through its whole reduction alone: with few workgroups their stages one after the other are the time, not
+// the weights' bytes (65 tokens of 7 experts, top_k = 2, K = 6144, I = 256, SwiGLU: 45 us for 32 MB).
 #include "dma.hpp"
 #include "half_gmm.hpp"
 
@@ -124,10 +126,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void h
     }
 }
 
-// Measured on both sides, this kernel and the 256-row tiles, in us, by mean rows an expert.  K = 7168, I = 2048, E = 32:
-// first product 1 row 186 / 246, 4 298 / 309, 16 317 / 318, 32 346 / 355, 40 335 / 333, 64 538 / 331; second product
-// 112 / 130, 155 / 196, 155 / 182, 190 / 233, 185 / 237, 243 / 197.  K = 4096, I = 1408, E = 64, Zipf(1.2) routing: 28
-// rows 304 / 321 and 157 / 168, 38 rows 343 / 316 and 173 / 170.
+// Measured on both sides, this kernel and the 256-row tiles, in us, by mean rows an expert.  K = 7168, I = 2048, E = 32,
+// uniform routing: first product with SwiGLU 1 row 250 / 265, 4 284 / 309, 16 280 / 298, 32 288 / 312, 40 293 / 310, 50
+// 295 / 305, 64 484 / 321; second product 122 / 137, 152 / 190, 157 / 185, 158 / 171, 161 / 173, 170 / 191, 242 / 185.  K
+// = 4096, I = 1408, E = 64, Zipf(1.2) routing, whose largest groups have several times the mean: 28 rows 264 / 286 and
+// 137 / 148, 32 rows 269 / 289 and 154 / 162, 36 rows 293 / 292 and 166 / 163, 38 rows 286 / 284 and 162 / 158.  The
+// bound is the skewed routing's: even groups would pay up to 64 rows, the second block of rows.
 bool half_few_ok(const HalfGmmParams &p) { return (p.R + p.E - 1) / p.E <= 36; }
 
 template <int T, bool SWIGLU, int NP>
@@ -138,7 +142,9 @@ static void few_launch(const HalfGmmParams &p, hipStream_t stream) {
 }
 
 hipError_t launch_half_few(const HalfGmmParams &p, int type, hipStream_t stream) {
-    // 32 or 64 rows a tile: mean 16 rows 304 / 305 us and 165 / 166, 32 rows 431 / 312 and 244 / 182, one token 70 / 71
+    // 32 or 64 rows a tile, us of the first product with SwiGLU and of the second, K = 7168, I = 2048, E = 32: one token
+    // 72 / 73 and 40 / 41, mean 1 row 251 / 254 and 123 / 125, 4 rows 299 / 284 and 152 / 156, 16 rows 291 / 280 and 157
+    // / 158, 32 rows 413 / 288 and 218 / 158
     const bool one = (p.R + p.E - 1) / p.E <= 16;
 #define FEW(T, S)                              \
     if (one) few_launch<T, S, 1>(p, stream);   \

@@ -38,7 +38,8 @@ namespace megamoe {
 // tiles, so that a tile's first stages are there when the tile before has been rounded and stored.
 //
 // K = 7168, I = 2048, E = 32, top_k = 8, bf16, random operands: first product of 2048 tokens 806 to 850 us, 1130 to 1190
-// TFLOP/s, of 16384 tokens 5680, 1355; its row gradient of 2048 tokens 850, its weight gradient 1000 to 1040.  An
+// TFLOP/s, of 16384 tokens 5680, 1355; its row gradient of 2048 tokens 850, its weight gradient 1000 to 1040.  Second product 466,
+// 1030 TFLOP/s, as its tiles are 32 stages and end 3.5 times as often.  An
 // 8192^3 library product reaches 1390 TFLOP/s here in bf16.  What bounds the products is power: at 2048 tokens the
 // card runs them at 1.63 of 2.4 GHz, with the matrix cores busy in 71% of the cycles.  Timed with work left out: without
 // copies 1.23 times as fast, the same cache lines copied in every stage 1.06, without stores no faster, without LDS reads
@@ -497,7 +498,8 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
         }
     };
     if (G::WEIGHTS && p.c_type == kFp32) {
-        // four columns a lane; stored as the 16-bit weights below (64 groups of 384 rows, 4096 x 1408: 517 us for 572)
+        // four columns a lane; stored as the 16-bit weights below (64 groups of 384 rows, 4096 x 1408: 490 to 517 us for
+        // 572).  Added: 1360 us, as a piece is loaded, waited for with all that is under way, and stored before the next
 #pragma unroll
         for (int i = 0; i < 2 * NP; ++i) {
 #pragma unroll
@@ -523,7 +525,8 @@ __device__ __forceinline__ void HgRun<G>::multiply_tile(const HgTile &t, int k) 
         }
         return;
     }
-    if (G::WEIGHTS && p.accumulate) {  // four columns a lane, added to what is there
+    // four columns a lane, added to what is there, a piece after the other as in fp32 (the same groups: 810 us, written 394)
+    if (G::WEIGHTS && p.accumulate) {
 #pragma unroll
         for (int i = 0; i < 2 * NP; ++i) {
             __builtin_amdgcn_sched_barrier(0);

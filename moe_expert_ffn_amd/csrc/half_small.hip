@@ -224,12 +224,18 @@ static long long small_tiles(const HalfGmmParams &p, int kind) {  // at most
     return ((long long)p.R / kSmallRows + (p.E < p.R ? p.E : p.R)) * (p.N / (kSmallCols / (p.swiglu ? 2 : 1)));
 }
 
-// Measured on both sides, the 256-row tiles and this kernel, in us, by the number of small tiles at 256 CUs.  Row gradients: 18 tiles
-// (28 rows, K = 5504) 74 / 20, 374 (100 rows, K = 6784, N = 1408) 103 / 50, 504 (3440 rows, K = 2560) 56 / 34, 616 (102 rows, K
-// = 768) 19 / 13, 688 37 / 28, 756 16 / 17, 1122 17 / 21, 1480 66 / 100.  Weights' gradients: 280 20 / 8, 896 (7965 rows) 33 / 23,
-// 1056 16 / 15, 1232 21 / 16, 1536 26 / 37 at three stages.  Products: 88 (318 rows, K = 2560) 45 / 26, 344 52 / 27, 436 46 / 41,
-// 496 61 / 55, 576 75 / 74, 640 102 / 136.  Products of few rows an expert have a kernel that is mostly faster than both: 39
-// us for 632 rows of 18 experts, K = 1280, N = 3328, and 87 here.
+// Measured on both sides, the 256-row tiles and this kernel, in us, by the number of small tiles (rows, reduction) at 256
+// CUs. Row gradients: 72 tiles (42 rows, 1024) 21 / 9, 150 (342, 4864) 76 / 27, 440 (2312, 768) 21 / 18, 616 (4220, 7040)
+// 133 / 107, 656 (10002, 1152) 32 / 32, 728 (1043, 768) 20 / 18, 788 (8919, 5248) 108 / 86, 936 (8182, 384) 20 / 25, 1050
+// (6412, 1280) 22 / 32, 1300 (45 rows of 26 experts, 1280) 50 / 38, 1428 (224, 1792) 39 / 44, 1860 (3174, 3840) 84 / 144:
+// past the bound this kernel is ahead for a few rows an expert and behind for many.  Weights' gradients, whose rows are
+// the reduction: 216 (9548 rows) 38 / 14, 504 (10705) 61 / 29, 672 (132) 15 / 11, 900 (5145) 35 / 33, 1040 (1344) 17 /
+// 16, 1064 (21344) 57 / 58, 1200 (15488) 66 / 39, 1280 (63) 14 / 15, 1536 (66) 15 / 16, 2016 (2580) 23 / 37, 2208 (10) 15
+// / 24: from the bound to some 1800 either.  Products: 188 (2694, 7552) 141 / 61, 296 (3330, 6784) 127 / 57, 368 (5598,
+// 1152) 31 / 29, 450 (4060, 1920) 43 / 39, 468 (816, 1024) 25 / 27, 512 (6645, 896) 27 / 25, 576 (595, 1152) 25 / 29, 640
+// (639, 2048) 37 / 39, 728 (5628, 256) 17 / 25, 816 (544, 2432) 47 / 67.  Products of few rows an expert have a kernel
+// that is mostly faster than both: 30 us for 632 rows of 18 experts, K = 1280, N = 3328, and 52 here; one token of K =
+// 7168, E = 32, top_k = 8, I = 256 37 us and 37 here, its second product 7 and 19, 16 such tokens 46 and 42.
 bool half_small_ok(const HalfGmmParams &p, int kind, int cu_count) {
     const long long halves = kind == kHalfProduct ? 4 : kind == kHalfRows ? 5 : 8;  // of tiles, a CU
     return 2 * small_tiles(p, kind) <= halves * cu_count && (kind != kHalfProduct || !half_few_ok(p));

@@ -156,12 +156,17 @@ __global__ __launch_bounds__(THREADS) void norm_kernel(NormParams p) {
     }
 }
 
-// Backwards.  A workgroup goes on to further tokens and keeps its sums over them for every column; they
-// go to the workspace, and a second kernel adds them up in a fixed order.  What it waits for is memory: a token's
-// rows are asked for together, and kept as they are stored until both of the token's reductions are done.  Sixteen
-// waves a CU, at 128 registers, hide more of the wait than eight that spill none of them (115 us for 95 below).
-// 4096 tokens of 4096 columns, six bf16 rows each, a gate a column: 365 MB in 92 us, 4.0 TB/s; the second kernel has
-// 6 us of it.  8192 tokens of 4096 columns, one norm: 604 MB in 126 us, 4.8 TB/s.
+// Backwards.  A workgroup goes on to further tokens and keeps its sums over them for every column; they go to the
+// workspace, and a second kernel adds them up in a fixed order.  What it waits for is memory: a token's rows are asked
+// for together, and kept as they are stored until both of the token's reductions are done.  Sixteen waves a CU, at 128
+// registers of which 24 to 29 spill, hide more of the wait than eight that spill none (112 us for 95 below). 4096 tokens
+// of 4096 columns, six bf16 rows each, a gate a column: 365 MB in 92 to 96 us, 3.9 TB/s; the second kernel has 6 us of
+// it.  bf16 and the norm before alone: 8192 tokens of 4096 columns 268 MB in 66 us, 4.1 TB/s.  Away from that it is far
+// from a copy's rate.  Few tokens: two kernels, one waiting for the other: 64 of 5376 columns 12 us for 3 MB, 390 16 us
+// for 17.  Few columns, where a CU has few waves (norm_grad_groups): 8192 tokens of 1024 33 us, 2.0 TB/s, 4000 of 384 16
+// us, 0.8.  Above 8192 columns a thread has two or four chunks, and the three sums of each column spill (122 to 210
+// registers, 381 to 495): 1000 tokens of 16384 columns 75 us, 1.8 TB/s, of 32768 197 us, 1.3 (with both norms and two
+// rows each 130, 1.8, and 398, 1.2).
 template <int TX, int TB, int C>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(NormParams p) {
     __shared__ float s_a[2][48], s_b[2][32];
@@ -322,8 +327,9 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormParams p, int n)
 static int norm_threads(int K, int C) { return ((K / 8 + C - 1) / C + 63) / 64 * 64; }
 static int norm_grad_c(int K) { return K <= 8192 ? 1 : K <= 16384 ? 2 : 4; }
 
-// Sixteen waves a CU at any K: with 512 workgroups always, of at most 512 threads, 8192 tokens of 2048 columns took
-// 113 us for 91, and 4096 of 7168 columns 223 for 209 (16384 columns, whose sums spill, 261 for 271).
+// At most sixteen waves a CU, which their registers allow: nine to sixteen from K = 1152 on, four to eight for a K of
+// 1024 and less, whose workgroups are one or two waves.  With 512 workgroups always, of at most 512 threads, 8192 tokens
+// of 2048 columns took 113 us for 91, and 4096 of 7168 columns 223 for 209.
 int norm_grad_groups(int M, int K) {
     const int threads = norm_threads(K, norm_grad_c(K)), most = threads > 512 ? 256 : threads > 256 ? 512 : 1024;
     return M < most ? M : most;
