@@ -93,7 +93,9 @@ int megamoe_half_swiglu_grad(const megamoe_dims *d, const uint16_t *c, const uin
  *   r    = x + alpha * gate * n; x null: 0, rows null: r = x, gate null: 1
  *   h    = r / sqrt(mean r^2 + eps) * w_before
  * Each of s, r, h is rounded from fp32 values that were not rounded before; every
- * one may be null (h exactly where w_before is), not all of them.  With rows alone r
+ * one may be null (h exactly where w_before is), not all of them.  Squares are in
+ * fp32 too: where a row's mean square passes its range (values of some 1e19), the
+ * norm of that row is 0.  With rows alone r
  * is the plain combine, with x and w_before alone h is the norm before a layer.
  *   x, r      x_type [M, K]; r may be x's own memory
  *   rows, s   rows_type [R, K] with expanded_row_idx [R], else [M, K]
