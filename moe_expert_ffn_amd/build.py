@@ -143,7 +143,7 @@ def check_half_kernels(remarks: str, srcs: list[str]) -> list[str]:
                 if not any(k in name for name in names)]
     for src in srcs:
         with open(src) as f:
-            declared = re.findall(r"__global__[^;{]*?\b(\w+)\(HalfGmmParams", f.read())
+            declared = re.findall(r"__global__[^;{]*?\b(\w+)\s*\(\s*(?:const\s+)?HalfGmmParams", f.read())
         problems += [f"16-bit product {k}: not among the kernels that are checked" for k in declared
                      if k not in HALF_KERNELS]
     return problems

@@ -35,9 +35,10 @@ def test_a_kernel_that_is_not_reported_fails(name):
     assert len(problems) == 1 and "not in the resource report" in problems[0]
 
 
-def test_a_kernel_under_another_name_fails(tmp_path):
+@pytest.mark.parametrize("arguments", ["(HalfGmmParams p)", "(const HalfGmmParams p, int n)", " (\n    HalfGmmParams p)"])
+def test_a_kernel_under_another_name_fails(tmp_path, arguments):
     src = tmp_path / "half_other.hip"
-    src.write_text("template <int T>\n__global__ __launch_bounds__(256) void half_other_kernel(HalfGmmParams p) {}\n")
+    src.write_text(f"template <int T>\n__global__ __launch_bounds__(256) void half_other_kernel{arguments} {{}}\n")
     problems = B.check_half_kernels(report(*ALL), SRCS + [str(src)])
     assert len(problems) == 1 and "half_other_kernel" in problems[0]
 
