@@ -258,7 +258,8 @@ class MegaMoEHalf:
     caller's tensors: what an optimiser writes to them is what the next call multiplies with.
 
     forward serves.  forward_rows and backward train: a token's output is the sum of its rows, which
-    combine gives, or megamoe_norm on its way through the norm after the layer."""
+    combine gives, or megamoe_norm on its way through the norm after the layer.  forward and forward_rows
+    share the workspace: calls of one holder belong in one order."""
 
     def __init__(self, M: int, K: int, E: int, top_k: int, I: int, dtype=torch.bfloat16, device="cuda"):
         self.d = dims(M, K, E, top_k, I)
@@ -291,8 +292,8 @@ class MegaMoEHalf:
         return out
 
     def forward_rows(self, x, expert_idx, probs) -> HalfPass:
-        """The layer up to the combine, keeping what backward needs.  Rows behind the last group are not
-        written."""
+        """The layer up to the combine, keeping what backward needs: x and probs themselves, which have to
+        hold the same values then.  Rows behind the last group are not written."""
         d, i32 = self.d, torch.int32
         R = d.M * d.top_k
         row_of, route = self._empty(R, dtype=i32), self._empty(R, dtype=i32)
@@ -316,7 +317,7 @@ class MegaMoEHalf:
     def backward(self, p: HalfPass, dout, dw1=None, dw2=None, accumulate=False):
         """dout [M, K], the gradient of the combined output -> dx_rows [R, K] (combine sums them to x's),
         dprobs [M, top_k], dw1, dw2.  dw1 and dw2: where the weights' gradients go, of the weights' type
-        or fp32, to be added to with accumulate."""
+        or fp32, to be added to with accumulate.  Rows of dx_rows behind the last group are not written."""
         if accumulate and (dw1 is None or dw2 is None):
             raise ValueError("accumulate adds to dw1 and dw2, which have to be given")
         d = self.d
