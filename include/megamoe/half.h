@@ -5,10 +5,11 @@
  *
  * The conventions, dims, limits, types and errors are those of megamoe.h.  `type` is
  * MEGAMOE_FP16 or MEGAMOE_BF16, one for all 16-bit tensors of a call; sums and
- * statistics are in fp32 and rounded once, at the end.  No result depends on timing.
- * Rows of the expert-major order at and past the last element of expert_cumsum are
- * left as they are.  Weights are rows over the forward's reduction, with no further
- * layout:
+ * statistics are in fp32 and rounded once, at the end.  (In the products' sums a
+ * subnormal fp16 value counts, to the accuracy that 2^-14 in its place would have.)
+ * No result depends on timing.  Rows of the expert-major order at and past the last
+ * element of expert_cumsum are left as they are.  Weights are rows over the forward's
+ * reduction, with no further layout:
  *   w1 [E, 2I, K]  rows [0, I) feed silu, [I, 2I) the gate
  *   w2 [E, K, I]
  */

@@ -30,6 +30,9 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 // either operand lane l has row l & 15 and 8 (l >> 4) + 0..7 of the reduction.  (From registers, on random operands,
 // for which the card lowers its clock, it ran at 2030 TFLOP/s and the 32 x 32 x 16 form at 1730, as that one
 // goes through its sums twice as often; on zeros 2420 and 2470.)
+// A subnormal fp16 operand is taken as it is stored, 0.f 2^-14, and its product aligned to that: it counts, but no more exactly
+// than if the operand were 2^-14 (five products of 2^-21 with values up to 2.3 were off by 2^-37 together, where a step
+// of their sum in fp32 is 2^-43).
 template <int T>
 __device__ __forceinline__ v4f hg_mfma(v4i w, v4i a, v4f acc) {
     if constexpr (T == kBf16)
